@@ -31,6 +31,13 @@
  *                            act = silu(gate) * up
  *   moe_swiglu_backward      gradients of the activation
  *
+ * and the router in front of the plan:
+ *
+ *   moe_router           logits to topk_ids and gates, with the balance loss
+ *                        and per-expert counts of every sequence if wanted
+ *   moe_balance_loss     that loss for ids chosen elsewhere
+ *   moe_router_backward  gradients of gates and loss by the logits
+ *
  * Prefetch pool ("Moonshot AI 开源 MoonEP", 核心思想: the prefetch slots come
  * from one rank-global pool shared by all layers, so the extra memory is B
  * expert weights per projection in total, not per layer).  w_pref and
@@ -420,6 +427,88 @@ int moe_grouped_gemm_swiglu(const moe_cfg *cfg, const moe_bf16 *xperm,
  */
 int moe_swiglu_backward(const moe_cfg *cfg, const moe_bf16 *h13, const moe_bf16 *dact,
                         moe_bf16 *dh13, hipStream_t stream);
+
+/* Score functions of the router. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+#define MOE_MAX_NSEQ (1 << 20)
+
+/*
+ * Router settings.  Tokens, experts and K come from the moe_cfg (its H, Hp, B
+ * and mode are checked as everywhere and not used): T = R*S tokens.
+ * Requirements: a known score, flags 0 or 1, 1 <= nseq <= MOE_MAX_NSEQ
+ * (MOE_ELIMIT above).
+ */
+typedef struct {
+  int32_t score;       /* MOE_SCORE_*                                        */
+  int32_t renormalize; /* 1: a token's K gates are divided by their sum       */
+  float scale;         /* factor on every gate                               */
+  int32_t logits_bf16; /* logits and dlogits are bf16 (1) or fp32 (0)         */
+  int32_t nseq;        /* sequences of the balance loss                      */
+} moe_router_cfg;
+
+/* Host only.  Bytes of the `workspace` of moe_router and moe_balance_loss. */
+int moe_router_workspace_size(const moe_cfg *cfg, const moe_router_cfg *rcfg, size_t *bytes_out);
+
+/*
+ * Router ("大规模 LLM 训练系统研究账本" §6.1: the router's top-K precedes
+ * dispatch, and its weights sum the expert outputs).  logits [R*S][E], one
+ * token's being z, score s = softmax(z) or s_e = 1 / (1 + e^-z_e):
+ *   topk_ids[t] = the K experts of the largest z_e (bias NULL) or of
+ *                 s_e + bias_e in float64, largest first, equal ones in
+ *                 ascending id; K distinct experts always
+ *   gates[t][k] = scale * s_id, divided by the sum of the token's K chosen
+ *                 scores if renormalize.  The bias takes part in the choice
+ *                 only.
+ * bias [E] fp32 or NULL, topk_ids [R*S][K] int32 and gates [R*S][K] fp32 as
+ * moe_plan_run and moe_combine take them.  A logit of -inf masks an expert:
+ * its score is 0 and it is chosen after all others; a row of nothing else gets
+ * the lowest ids and gates of 0.  A NaN logit is chosen last of all; NaN and
+ * +inf pass through the sums they enter as IEEE arithmetic has it.
+ *
+ * Balance loss (with counts, prob and loss given; all three or none).  Tokens
+ * cu_tokens[q] .. cu_tokens[q + 1] - 1 are sequence q, 0 <= q < nseq
+ * (cu_tokens [nseq+1] int32, ascending, within [0, R*S]; NULL with nseq 1:
+ * every token).  With p = softmax(z), or s / (sum of its E scores), and L the
+ * sequence's length:
+ *   counts[q][e] = routes of the sequence's tokens to expert e     (int32)
+ *   prob[q][e]   = mean of p_e over the sequence                   (fp32)
+ *   loss[q]      = sum_e E * counts[q][e] / (K * L) * prob[q][e]   (fp32)
+ * An empty sequence has zeros.  Tokens of no sequence are routed and take no
+ * part in the loss.  A row of -inf alone has p = 0.  The sums run in a fixed
+ * order: the same inputs give bit-identical outputs.  workspace (only with the
+ * loss): moe_router_workspace_size() bytes; concurrent calls need distinct
+ * ones.
+ */
+int moe_router(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
+               const float *bias, int32_t *topk_ids, float *gates, const int32_t *cu_tokens,
+               int32_t *counts, float *prob, float *loss, void *workspace, hipStream_t stream);
+
+/*
+ * The balance loss of moe_router for given topk_ids [R*S][K] (a router of the
+ * caller's own).  An id outside [0, E) is not counted; one named twice by a
+ * token counts twice.
+ */
+int moe_balance_loss(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
+                     const int32_t *topk_ids, const int32_t *cu_tokens, int32_t *counts,
+                     float *prob, float *loss, void *workspace, hipStream_t stream);
+
+/*
+ * Gradients by the logits of the gates (dgates [R*S][K] fp32 given), of the
+ * balance loss (dloss [nseq] fp32 given, with the forward's counts and
+ * cu_tokens), or of both:
+ *   dlogits[t] = sum_k dgates[t][k] d gates[t][k] / d z
+ *              + dloss[q] d loss[q] / d z
+ * The choice of experts and the counts are constants.  Written whole, rounded
+ * once, in the logits' type; a token of no sequence has no second part.  An id
+ * outside [0, E) contributes nothing.  dlogits may be logits (in place).
+ * topk_ids is read only with dgates, counts and cu_tokens only with dloss; at
+ * least one of dgates and dloss is given.
+ */
+int moe_router_backward(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
+                        const int32_t *topk_ids, const float *dgates, const int32_t *cu_tokens,
+                        const int32_t *counts, const float *dloss, void *dlogits,
+                        hipStream_t stream);
 
 /* Host only.  Static text for a MOE_* return code. */
 const char *moe_strerror(int code);

@@ -17,6 +17,7 @@ MOE_OK, MOE_EINVAL, MOE_EHIP, MOE_ELIMIT = 0, -1, -2, -3
 MODE_TRAIN, MODE_INFER = 0, 1
 STATUS_BAD_ID, STATUS_UNBALANCED, STATUS_CAPACITY, STATUS_INTERNAL = 1, 2, 4, 8
 PLAN_ASCENDING, PLAN_LARGEST_FIRST = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 PLAN_FIELDS = ("counts", "load0", "route", "cu_seqlens", "slot_expert",
                "n_redundant", "src_rank", "moves", "status", "workspace")
 ENTRY_POINTS = ("moe_plan_sizes", "moe_plan_run", "moe_plan_run_policy", "moe_prefetch_weight",
@@ -25,7 +26,9 @@ ENTRY_POINTS = ("moe_plan_sizes", "moe_plan_run", "moe_plan_run_policy", "moe_pr
                 "moe_combine", "moe_grouped_gemm_wgrad", "moe_reduce_grad",
                 "moe_combine_backward", "moe_grouped_gemm_dgrad",
                 "moe_dispatch_backward", "moe_route_encode", "moe_dispatch_dedup",
-                "moe_grouped_gemm_swiglu", "moe_swiglu_backward", "moe_strerror")
+                "moe_grouped_gemm_swiglu", "moe_swiglu_backward",
+                "moe_router_workspace_size", "moe_router", "moe_balance_loss",
+                "moe_router_backward", "moe_strerror")
 
 
 class MoeError(RuntimeError):
@@ -39,6 +42,12 @@ class moe_cfg(ctypes.Structure):
 
     def __repr__(self):
         return "moe_cfg(%s)" % ", ".join("%s=%d" % (n, getattr(self, n)) for n, _ in self._fields_)
+
+
+class moe_router_cfg(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("logits_bf16", ctypes.c_int32),
+                ("nseq", ctypes.c_int32)]
 
 
 class moe_plan(ctypes.Structure):
@@ -61,6 +70,7 @@ def load(path=None):
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     C = ctypes.POINTER(moe_cfg)
     PL = ctypes.POINTER(moe_plan)
+    RC = ctypes.POINTER(moe_router_cfg)
     sig = {
         "moe_plan_sizes": [C, ctypes.POINTER(SZ)],
         "moe_plan_run": [C, P, PL, P],
@@ -80,6 +90,10 @@ def load(path=None):
         "moe_dispatch_dedup": [C, P, P, P, P],
         "moe_grouped_gemm_swiglu": [C, P, P, P, P, P, P, I32, I32, P, P],
         "moe_swiglu_backward": [C, P, P, P, P],
+        "moe_router_workspace_size": [C, RC, ctypes.POINTER(SZ)],
+        "moe_router": [C, RC, P, P, P, P, P, P, P, P, P, P],
+        "moe_balance_loss": [C, RC, P, P, P, P, P, P, P, P],
+        "moe_router_backward": [C, RC, P, P, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -120,6 +134,14 @@ def _ptr(t, dtype, numel=None, name="tensor"):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on_device(*tensors):
+    """Refuse tensors of another GPU than the current one (the launch's)."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, here))
 
 
 def moe_strerror(code):
@@ -345,3 +367,66 @@ def moe_reduce_grad(cfg, plan, grad_home, grad_pref, stream=None):
     b = _ptr(grad_pref, torch.float32, cfg.R * cfg.B * hh, "grad_pref") if cfg.B else None
     _check(load().moe_reduce_grad(ctypes.byref(cfg), plan.c, a, b, _stream(stream)),
            "moe_reduce_grad")
+
+
+def make_router_cfg(score, renormalize, scale=1.0, logits_bf16=False, nseq=1):
+    return moe_router_cfg(int(score), int(renormalize), float(scale), int(logits_bf16), int(nseq))
+
+
+def moe_router_workspace_size(cfg, rcfg):
+    out = ctypes.c_size_t()
+    _check(load().moe_router_workspace_size(ctypes.byref(cfg), ctypes.byref(rcfg),
+                                            ctypes.byref(out)), "moe_router_workspace_size")
+    return int(out.value)
+
+
+def _logits(cfg, rcfg, t, name):
+    return _ptr(t, torch.bfloat16 if rcfg.logits_bf16 else torch.float32,
+                cfg.R * cfg.S * cfg.E, name)
+
+
+def _loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace):
+    n = rcfg.nseq
+    return (_ptr(cu_tokens, torch.int32, n + 1, "cu_tokens"),
+            _ptr(counts, torch.int32, n * cfg.E, "counts"),
+            _ptr(prob, torch.float32, n * cfg.E, "prob"),
+            _ptr(loss, torch.float32, n, "loss"),
+            _ptr(workspace, torch.uint8,
+                 moe_router_workspace_size(cfg, rcfg) if loss is not None else None, "workspace"))
+
+
+def moe_router(cfg, rcfg, logits, bias, topk_ids, gates, cu_tokens=None, counts=None, prob=None,
+               loss=None, workspace=None, stream=None):
+    """Ids and gates; with counts, prob, loss and workspace the balance loss too."""
+    n = cfg.R * cfg.S * cfg.K
+    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
+            _ptr(bias, torch.float32, cfg.E, "bias"),
+            _ptr(topk_ids, torch.int32, n, "topk_ids"),
+            _ptr(gates, torch.float32, n, "gates"),
+            *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace))
+    _on_device(logits, bias, topk_ids, gates, cu_tokens, counts, prob, loss, workspace)
+    _check(load().moe_router(*args, _stream(stream)), "moe_router")
+
+
+def moe_balance_loss(cfg, rcfg, logits, topk_ids, cu_tokens, counts, prob, loss, workspace,
+                     stream=None):
+    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
+            _ptr(topk_ids, torch.int32, cfg.R * cfg.S * cfg.K, "topk_ids"),
+            *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace))
+    _on_device(logits, topk_ids, cu_tokens, counts, prob, loss, workspace)
+    _check(load().moe_balance_loss(*args, _stream(stream)), "moe_balance_loss")
+
+
+def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits,
+                        stream=None):
+    """dgates or dloss (with counts and cu_tokens) may be None."""
+    n = cfg.R * cfg.S * cfg.K
+    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
+            _ptr(topk_ids, torch.int32, n, "topk_ids"),
+            _ptr(dgates, torch.float32, n, "dgates"),
+            _ptr(cu_tokens, torch.int32, rcfg.nseq + 1, "cu_tokens"),
+            _ptr(counts, torch.int32, rcfg.nseq * cfg.E, "counts"),
+            _ptr(dloss, torch.float32, rcfg.nseq, "dloss"),
+            _logits(cfg, rcfg, dlogits, "dlogits"))
+    _on_device(logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits)
+    _check(load().moe_router_backward(*args, _stream(stream)), "moe_router_backward")
