@@ -38,6 +38,15 @@
  *   moe_balance_loss     that loss for ids chosen elsewhere
  *   moe_router_backward  gradients of gates and loss by the logits
  *
+ * and the activations that the backward needs, kept in 8 bits:
+ *
+ *   moe_q8_store, moe_q8_load      bf16 rows to codes and scales, and back
+ *   moe_dispatch_q8                dispatch redone from the layer input's codes
+ *   moe_grouped_gemm_swiglu_q8     first projection that keeps h13 as codes
+ *   moe_swiglu_backward_q8         gradients of the activation from them, and
+ *                                  the activation again
+ *   moe_combine_backward_q8        gradients of combine from y's codes
+ *
  * Prefetch pool ("Moonshot AI 开源 MoonEP", 核心思想: the prefetch slots come
  * from one rank-global pool shared by all layers, so the extra memory is B
  * expert weights per projection in total, not per layer).  w_pref and
@@ -509,6 +518,74 @@ int moe_router_backward(const moe_cfg *cfg, const moe_router_cfg *rcfg, const vo
                         const int32_t *topk_ids, const float *dgates, const int32_t *cu_tokens,
                         const int32_t *counts, const float *dloss, void *dlogits,
                         hipStream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits ("大规模 LLM 训练系统研究账本" §9.5: the
+ * backward keeps what dispatch laid out or redoes it; here what it keeps takes
+ * half the bytes).  A row of `width` bf16 values is cut into blocks of 32
+ * consecutive ones (the last block may be shorter).  A block's scale is 2^k
+ * with the least k >= -127 such that its largest finite magnitude is at most
+ * 448 * 2^k; a value's code is the e4m3 number (OCP FP8: 4 exponent bits, bias
+ * 7, 3 mantissa bits, no infinity) nearest to value / 2^k, ties to even.  So a
+ * kept value is off by at most 2^-4 of itself, or by 2^(k-10) below 2^(k-6).
+ * A value that is not finite becomes NaN and takes no part in the scale.
+ *   q     [rows][width] uint8, the codes (base on a 16-byte boundary)
+ *   scale [rows][ceil(width/32)] uint8, k + 127
+ * What a code stands for, code * 2^k, is exact in bf16.
+ * width % 8 == 0, width >= 8, rows >= 0; rows * ceil(width/32) * 32 < 2^37
+ * (MOE_ELIMIT).
+ */
+int moe_q8_store(int64_t rows, int32_t width, const moe_bf16 *src, uint8_t *q, uint8_t *scale,
+                 hipStream_t stream);
+
+/*
+ * dst [rows][width] bf16 = the values that q and scale stand for (exact for
+ * what moe_q8_store writes; a code of other origin that passes bf16's range is
+ * infinite, one below its last place is cut off).
+ */
+int moe_q8_load(int64_t rows, int32_t width, const uint8_t *q, const uint8_t *scale,
+                moe_bf16 *dst, hipStream_t stream);
+
+/*
+ * moe_dispatch of a layer input kept in 8 bits: xperm[route[t*K + k]] = the
+ * values of row t of (xq, xscale), bit for bit those of moe_q8_load.  xq
+ * [R*S][H], xscale [R*S][ceil(H/32)] as moe_q8_store(R*S, H, ...) writes them.
+ */
+int moe_dispatch_q8(const moe_cfg *cfg, const moe_plan *plan, const uint8_t *xq,
+                    const uint8_t *xscale, moe_bf16 *xperm, hipStream_t stream);
+
+/*
+ * moe_grouped_gemm_swiglu that keeps h13 = [bf16(gate) | bf16(up)] in 8 bits:
+ * h13q [R][S*K][2H'] and h13scale [R][S*K][2][ceil(H'/32)] are bit for bit
+ * what moe_q8_store(2*R*S*K, H', h13, ...) makes of that call's h13 (gate and
+ * up have blocks of their own).  act as there.  Rows outside the listed ranks
+ * are not written.
+ */
+int moe_grouped_gemm_swiglu_q8(const moe_cfg *cfg, const moe_bf16 *xperm,
+                               const moe_bf16 *w13_home, const moe_bf16 *w13_pref,
+                               const int32_t *cu_seqlens, moe_bf16 *act, uint8_t *h13q,
+                               uint8_t *h13scale, int32_t rank_begin, int32_t rank_end,
+                               void *workspace, hipStream_t stream);
+
+/*
+ * moe_swiglu_backward from the kept h13 (layout as moe_grouped_gemm_swiglu_q8
+ * writes it), with gate and up the values it stands for.  If act is not NULL,
+ * also act = bf16(silu(gate) * up) [R][S*K][H'] of those values, so that the
+ * second projection's weight gradient needs no activation kept from the
+ * forward.  dh13 and act must not overlap the inputs or each other, except
+ * that act may be dact (in place).
+ */
+int moe_swiglu_backward_q8(const moe_cfg *cfg, const uint8_t *h13q, const uint8_t *h13scale,
+                           const moe_bf16 *dact, moe_bf16 *dh13, moe_bf16 *act,
+                           hipStream_t stream);
+
+/*
+ * moe_combine_backward from y kept in 8 bits (moe_q8_store(R*S*K, H', y,
+ * ...)): dy as there, dgates with the values that the codes stand for.
+ */
+int moe_combine_backward_q8(const moe_cfg *cfg, const moe_plan *plan, const moe_bf16 *dout,
+                            const uint8_t *yq, const uint8_t *yscale, const float *gates,
+                            moe_bf16 *dy, float *dgates, hipStream_t stream);
 
 /* Host only.  Static text for a MOE_* return code. */
 const char *moe_strerror(int code);

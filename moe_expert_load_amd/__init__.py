@@ -28,7 +28,9 @@ ENTRY_POINTS = ("moe_plan_sizes", "moe_plan_run", "moe_plan_run_policy", "moe_pr
                 "moe_dispatch_backward", "moe_route_encode", "moe_dispatch_dedup",
                 "moe_grouped_gemm_swiglu", "moe_swiglu_backward",
                 "moe_router_workspace_size", "moe_router", "moe_balance_loss",
-                "moe_router_backward", "moe_strerror")
+                "moe_router_backward", "moe_q8_store", "moe_q8_load", "moe_dispatch_q8",
+                "moe_grouped_gemm_swiglu_q8", "moe_swiglu_backward_q8",
+                "moe_combine_backward_q8", "moe_strerror")
 
 
 class MoeError(RuntimeError):
@@ -67,7 +69,7 @@ def load(path=None):
         raise RuntimeError("MoonEP HIP library not built: %s is missing "
                            "(run python -m moe_expert_load_amd.build)" % p)
     lib = ctypes.CDLL(p)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(moe_cfg)
     PL = ctypes.POINTER(moe_plan)
     RC = ctypes.POINTER(moe_router_cfg)
@@ -94,6 +96,12 @@ def load(path=None):
         "moe_router": [C, RC, P, P, P, P, P, P, P, P, P, P],
         "moe_balance_loss": [C, RC, P, P, P, P, P, P, P, P],
         "moe_router_backward": [C, RC, P, P, P, P, P, P, P, P],
+        "moe_q8_store": [I64, I32, P, P, P, P],
+        "moe_q8_load": [I64, I32, P, P, P, P],
+        "moe_dispatch_q8": [C, PL, P, P, P, P],
+        "moe_grouped_gemm_swiglu_q8": [C, P, P, P, P, P, P, P, I32, I32, P, P],
+        "moe_swiglu_backward_q8": [C, P, P, P, P, P, P],
+        "moe_combine_backward_q8": [C, PL, P, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -430,3 +438,74 @@ def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, 
             _logits(cfg, rcfg, dlogits, "dlogits"))
     _on_device(logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits)
     _check(load().moe_router_backward(*args, _stream(stream)), "moe_router_backward")
+
+
+def _kept(rows, width, q, scale, what):
+    """Codes and scale bytes of `rows` rows of `width` values."""
+    return (_ptr(q, torch.uint8, rows * width, what + " codes"),
+            _ptr(scale, torch.uint8, rows * ((width + 31) // 32), what + " scales"))
+
+
+def moe_q8_store(rows, width, src, q, scale, stream=None):
+    """Codes q [rows, width] and scale bytes [rows, ceil(width / 32)] of bf16 rows."""
+    a = _ptr(src, torch.bfloat16, rows * width, "src")
+    kept = _kept(rows, width, q, scale, "q8")
+    _on_device(src, q, scale)
+    _check(load().moe_q8_store(rows, width, a, *kept, _stream(stream)), "moe_q8_store")
+
+
+def moe_q8_load(rows, width, q, scale, dst, stream=None):
+    kept = _kept(rows, width, q, scale, "q8")
+    o = _ptr(dst, torch.bfloat16, rows * width, "dst")
+    _on_device(q, scale, dst)
+    _check(load().moe_q8_load(rows, width, *kept, o, _stream(stream)), "moe_q8_load")
+
+
+def moe_dispatch_q8(cfg, plan, xq, xscale, xperm, stream=None):
+    ntok = cfg.R * cfg.S
+    kept = _kept(ntok, cfg.H, xq, xscale, "x")
+    o = _ptr(xperm, torch.bfloat16, ntok * cfg.K * cfg.H, "xperm")
+    _on_device(plan.route, xq, xscale, xperm)
+    _check(load().moe_dispatch_q8(ctypes.byref(cfg), plan.c, *kept, o, _stream(stream)),
+           "moe_dispatch_q8")
+
+
+def moe_grouped_gemm_swiglu_q8(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, h13q, h13scale,
+                               rank_begin, rank_end, workspace, stream=None):
+    """cfg.Hp is the intermediate size H'; W13 rows are [H][2H'] (gate | up)."""
+    SK = cfg.S * cfg.K
+    hh = cfg.H * 2 * cfg.Hp
+    args = (ctypes.byref(cfg),
+            _ptr(xperm, torch.bfloat16, cfg.R * SK * cfg.H, "xperm"),
+            _ptr(w13_home, torch.bfloat16, cfg.E * hh, "w13_home"),
+            _ptr(w13_pref, torch.bfloat16, cfg.R * cfg.B * hh, "w13_pref") if cfg.B else None,
+            _ptr(cu_seqlens, torch.int32, cfg.R * (cfg.E + cfg.B + 1), "cu_seqlens"),
+            _ptr(act, torch.bfloat16, cfg.R * SK * cfg.Hp, "act"),
+            *_kept(2 * cfg.R * SK, cfg.Hp, h13q, h13scale, "h13"),
+            int(rank_begin), int(rank_end),
+            _ptr(workspace, torch.uint8, moe_gemm_workspace_size(cfg), "workspace"))
+    _on_device(xperm, w13_home, w13_pref, cu_seqlens, act, h13q, h13scale, workspace)
+    _check(load().moe_grouped_gemm_swiglu_q8(*args, _stream(stream)),
+           "moe_grouped_gemm_swiglu_q8")
+
+
+def moe_swiglu_backward_q8(cfg, h13q, h13scale, dact, dh13, act=None, stream=None):
+    rows = cfg.R * cfg.S * cfg.K
+    args = (ctypes.byref(cfg), *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13"),
+            _ptr(dact, torch.bfloat16, rows * cfg.Hp, "dact"),
+            _ptr(dh13, torch.bfloat16, rows * 2 * cfg.Hp, "dh13"),
+            _ptr(act, torch.bfloat16, rows * cfg.Hp, "act"))
+    _on_device(h13q, h13scale, dact, dh13, act)
+    _check(load().moe_swiglu_backward_q8(*args, _stream(stream)), "moe_swiglu_backward_q8")
+
+
+def moe_combine_backward_q8(cfg, plan, dout, yq, yscale, gates, dy, dgates, stream=None):
+    ntok = cfg.R * cfg.S
+    args = (ctypes.byref(cfg), plan.c,
+            _ptr(dout, torch.bfloat16, ntok * cfg.Hp, "dout"),
+            *_kept(ntok * cfg.K, cfg.Hp, yq, yscale, "y"),
+            _ptr(gates, torch.float32, ntok * cfg.K, "gates"),
+            _ptr(dy, torch.bfloat16, ntok * cfg.K * cfg.Hp, "dy"),
+            _ptr(dgates, torch.float32, ntok * cfg.K, "dgates"))
+    _on_device(plan.route, dout, yq, yscale, gates, dy, dgates)
+    _check(load().moe_combine_backward_q8(*args, _stream(stream)), "moe_combine_backward_q8")

@@ -29,7 +29,8 @@
 //   W_up] in one [E+B, H, 2H'] tensor -- each 256-column tile takes 128
 //   gate and the same 128 up columns, interleaved in 32-column blocks, so
 //   every wave holds gate and up of the same outputs in its accumulators
-//   and applies the activation in registers.
+//   and applies the activation in registers; MODE 4: the same, with gate
+//   and up kept as 8-bit codes (q8.hpp) instead of bf16.
 // Tile: BM = BN = 256, BK = 32; 4 waves in a 2x2 grid, each 128x128 =
 // 4x4 MFMA blocks of 32x32 with fp32 accumulators (256 AGPRs per wave).
 // Operands go from global memory straight into LDS (buffer_load ... lds,
@@ -52,6 +53,7 @@
 
 #include "common.hpp"
 #include "host.hpp"
+#include "q8.hpp"
 
 namespace moonep {
 
@@ -84,7 +86,7 @@ constexpr int kABlock = 64;     // rows between a wave's row blocks
 #endif
 constexpr int kBand = MOONEP_GEMM_BAND;
 
-enum { MODE_FWD = 0, MODE_WGRAD = 1, MODE_DGRAD = 2, MODE_SWIGLU = 3 };
+enum { MODE_FWD = 0, MODE_WGRAD = 1, MODE_DGRAD = 2, MODE_SWIGLU = 3, MODE_SWIGLU_Q8 = 4 };
 
 struct WorkItem {
   int32_t r, j, row0, rows;  // rank, weight row, first xperm row (absolute), row count
@@ -104,6 +106,8 @@ struct GemmArgs {
   const WorkItem* items;      // work list of this launch's tile class
   const int32_t* nitems;      // its item count
   int32_t H, Hp, E, B, SK;
+  uint8_t* h13q;              // MODE_SWIGLU_Q8: codes and scale bytes of gate and up
+  uint8_t* h13s;
 };
 
 // Cache-policy operand of the buffer-store builtin: non-temporal.
@@ -303,9 +307,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
   constexpr bool kRowB = MODE == MODE_DGRAD;
   // Paired A tiles wherever A is a row tile (forward, data gradient, SwiGLU
   // projection).
-  constexpr bool kPair = (MODE == MODE_FWD || MODE == MODE_DGRAD || MODE == MODE_SWIGLU) &&
+  constexpr bool kQ8 = MODE == MODE_SWIGLU_Q8;
+  constexpr bool kSwi = MODE == MODE_SWIGLU || kQ8;
+  constexpr bool kPair = (MODE == MODE_FWD || MODE == MODE_DGRAD || kSwi) &&
                          MOONEP_GEMM_PAIRA && BK == 32 && kNST == 4;
-  constexpr bool kSwi = MODE == MODE_SWIGLU;
   constexpr bool kNMajor =
       MODE == MODE_DGRAD || ((MODE == MODE_FWD || kSwi) && MOONEP_FWD_NMAJOR);
   const int H = g.H, Hp = g.Hp;
@@ -845,10 +850,16 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
       unsigned char* Ca = kPair ? (wv < 2 ? g_pa0 : g_pa1) + (wv & 1) * 16384 : epilogue_area(wv);
       unsigned char* Cg = epilogue_area2(wv);
       const int a0 = tn * (BN / 2) + wn * 64;
-      const bool keep = g.h13 != nullptr;
+      // MODE_SWIGLU_Q8 keeps the staged bf16 gate and up as codes: four lanes
+      // hold one row's block of 32 columns, so its scale is a maximum over
+      // them, and each 16-byte piece goes out as 8 bytes.
+      const bool keep = kQ8 || g.h13 != nullptr;
       const int nout = keep ? 3 * 64 * 8 : 64 * 8;
       uint16_t* actb = g.y + int64_t(it.row0) * Hp;
-      uint16_t* hb = keep ? g.h13 + int64_t(it.row0) * 2 * Hp : nullptr;
+      uint16_t* hb = keep && !kQ8 ? g.h13 + int64_t(it.row0) * 2 * Hp : nullptr;
+      const int sb = (Hp + kQ8Block - 1) / kQ8Block;
+      uint8_t* qb = kQ8 ? g.h13q + int64_t(it.row0) * 2 * Hp : nullptr;
+      uint8_t* qs = kQ8 ? g.h13s + int64_t(it.row0) * 2 * sb : nullptr;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int lo = 4 * (lane >> 5), col2 = (lane & 31) * 2;
@@ -882,6 +893,21 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
           const int n = a0 + cc * 8;
           const unsigned char* src = which == 0 ? Ca + rr * 144 + cc * 16
                                                 : Cg + (which - 1) * 8192 + rr * 128 + cc * 16;
+          if constexpr (kQ8) {
+            if (which > 0) {                             // uniform: 512 pieces each
+              const bool col = n < Hp;                   // columns past H' hold other weights
+              const u32x4 v = col ? *reinterpret_cast<const u32x4*>(src) : u32x4{0, 0, 0, 0};
+              const uint32_t b = q8_scale_byte(q8_group_max(q8_top(v)));
+              const q8_u32x2 code = q8_encode(v, b);
+              if (m < it.rows && col) {
+                *reinterpret_cast<q8_u32x2*>(qb + uint32_t(m) * 2 * Hp + (which - 1) * Hp + n) =
+                    code;
+                if ((cc & 3) == 0)
+                  qs[uint32_t(m) * 2 * sb + (which - 1) * sb + (n >> 5)] = (uint8_t)b;
+              }
+              continue;
+            }
+          }
           uint16_t* dst = which == 0 ? actb + uint32_t(m) * Hp + n
                                      : hb + uint32_t(m) * 2 * Hp + (which - 1) * Hp + n;
           if (m < it.rows && n < Hp)
@@ -1534,8 +1560,9 @@ static int launch_gemm(int mode, const moe_cfg* c, GemmArgs& g, SchedArgs& s, hi
   }
   const int kdepth = mode == MODE_DGRAD ? c->Hp : c->H;
   s.G = G;
-  s.ntn = mode == MODE_SWIGLU ? (c->Hp + BN / 2 - 1) / (BN / 2)
-                              : ((mode == MODE_DGRAD ? c->H : c->Hp) + BN - 1) / BN;
+  s.ntn = mode == MODE_SWIGLU || mode == MODE_SWIGLU_Q8
+              ? (c->Hp + BN / 2 - 1) / (BN / 2)
+              : ((mode == MODE_DGRAD ? c->H : c->Hp) + BN - 1) / BN;
   s.nk = ((kdepth + kBK - 1) / kBK + kNST - 1) / kNST * kNST;
   const CostModel& m = mode == MODE_DGRAD ? kCostDgrad : kCostFwd;
   s.c0 = m.tile; s.c1 = m.k; s.c2 = m.k_block; s.cL = m.launch;
@@ -1547,6 +1574,7 @@ static int launch_gemm(int mode, const moe_cfg* c, GemmArgs& g, SchedArgs& s, hi
   hipLaunchKernelGGL(k_sched<MODE_FWD>, dim3(1), dim3(1024), 0, stream, s);
   if (mode == MODE_FWD) launch_classes<MODE_FWD>(g, s, G, stream);
   else if (mode == MODE_SWIGLU) launch_classes<MODE_SWIGLU>(g, s, G, stream);
+  else if (mode == MODE_SWIGLU_Q8) launch_classes<MODE_SWIGLU_Q8>(g, s, G, stream);
   else launch_classes<MODE_DGRAD>(g, s, G, stream);
   return hip_status();
 }
@@ -1642,11 +1670,13 @@ extern "C" int moe_grouped_gemm_noalloc(const moe_cfg* cfg, const moe_bf16* xper
                           stream);
 }
 
-extern "C" int moe_grouped_gemm_swiglu(const moe_cfg* cfg, const moe_bf16* xperm,
-                                       const moe_bf16* w13_home, const moe_bf16* w13_pref,
-                                       const int32_t* cu_seqlens, moe_bf16* act, moe_bf16* h13,
-                                       int32_t rank_begin, int32_t rank_end, void* workspace,
-                                       hipStream_t stream) {
+// Checks and launch of the SwiGLU projection; h13 (bf16, optional) or h13q and
+// h13s (8-bit codes, if q8).
+static int swiglu_projection(const moe_cfg* cfg, const moe_bf16* xperm, const moe_bf16* w13_home,
+                             const moe_bf16* w13_pref, const int32_t* cu_seqlens, moe_bf16* act,
+                             moe_bf16* h13, uint8_t* h13q, uint8_t* h13s, bool q8,
+                             int32_t rank_begin, int32_t rank_end, void* workspace,
+                             hipStream_t stream) {
   const int rc = check_cfg(cfg);
   if (rc != MOE_OK) return rc;
   if (rank_begin < 0 || rank_end > cfg->R || rank_begin > rank_end) return MOE_EINVAL;
@@ -1655,12 +1685,32 @@ extern "C" int moe_grouped_gemm_swiglu(const moe_cfg* cfg, const moe_bf16* xperm
   if (rank_begin == rank_end || cfg->S == 0) return MOE_OK;
   if (!xperm || !w13_home || !cu_seqlens || !act || !workspace) return MOE_EINVAL;
   if (cfg->B > 0 && !w13_pref) return MOE_EINVAL;
+  if (q8 && (!h13q || !h13s || !aligned16(h13q))) return MOE_EINVAL;
   if (!aligned16(xperm, w13_home, w13_pref, act, h13, workspace)) return MOE_EINVAL;
   GemmArgs g{};
   g.xperm = xperm; g.w_home = w13_home; g.w_pref = w13_pref; g.y = act; g.h13 = h13;
+  g.h13q = h13q; g.h13s = h13s;
   g.H = cfg->H; g.Hp = cfg->Hp; g.E = cfg->E; g.B = cfg->B; g.SK = cfg->S * cfg->K;
   SchedArgs s = fwd_sched_args(cfg, cu_seqlens, workspace, rank_begin, rank_end);
-  return launch_gemm(MODE_SWIGLU, cfg, g, s, stream);
+  return launch_gemm(q8 ? MODE_SWIGLU_Q8 : MODE_SWIGLU, cfg, g, s, stream);
+}
+
+extern "C" int moe_grouped_gemm_swiglu(const moe_cfg* cfg, const moe_bf16* xperm,
+                                       const moe_bf16* w13_home, const moe_bf16* w13_pref,
+                                       const int32_t* cu_seqlens, moe_bf16* act, moe_bf16* h13,
+                                       int32_t rank_begin, int32_t rank_end, void* workspace,
+                                       hipStream_t stream) {
+  return swiglu_projection(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, h13, nullptr, nullptr,
+                           false, rank_begin, rank_end, workspace, stream);
+}
+
+extern "C" int moe_grouped_gemm_swiglu_q8(const moe_cfg* cfg, const moe_bf16* xperm,
+                                          const moe_bf16* w13_home, const moe_bf16* w13_pref,
+                                          const int32_t* cu_seqlens, moe_bf16* act,
+                                          uint8_t* h13q, uint8_t* h13scale, int32_t rank_begin,
+                                          int32_t rank_end, void* workspace, hipStream_t stream) {
+  return swiglu_projection(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, nullptr, h13q,
+                           h13scale, true, rank_begin, rank_end, workspace, stream);
 }
 
 extern "C" int moe_grouped_gemm_dgrad(const moe_cfg* cfg, const moe_bf16* dy, const moe_bf16* w_home,
