@@ -12,6 +12,7 @@
 // One wave holds one token's row: lane l has experts 128 j + 2 l and
 // 128 j + 2 l + 1, so a row of even E is read as pairs, and every reduction
 // over the experts is a DPP tree.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -19,7 +20,7 @@
 
 namespace moonep {
 
-constexpr int kRtThreads = 256;
+constexpr int kRtThreads = 512;
 constexpr int kRtWaves = kRtThreads / kWave;
 constexpr int kRtMaxChunks = 1024;              // workgroups whose sums are joined
 constexpr int kKeyNone = -2147483647 - 1;       // below every key: taken, or past E
@@ -44,6 +45,13 @@ __device__ __forceinline__ int expert_of(int i) {
   return ((i >> 1) << 7) + 2 * lane_id() + (i & 1);
 }
 
+// Two fp32 values as packed bf16, rounded to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // One logit, at any alignment.
 template <bool BF16>
 __device__ __forceinline__ float logit_at(const void* z, int64_t i) {
@@ -51,35 +59,54 @@ __device__ __forceinline__ float logit_at(const void* z, int64_t i) {
   else return reinterpret_cast<const float*>(z)[i];
 }
 
-// A row into P registers per lane; -inf (score 0) past E.
+// A token's row as loaded: P / 2 pairs per lane.  FULL: E == 64 P, every lane
+// holds P experts and nothing is masked.
 template <int P, bool BF16>
-__device__ __forceinline__ void load_row(const void* z, int64_t t, int E, float (&v)[P]) {
+struct Row {
+  uint32_t w[BF16 ? P / 2 : P];
+};
+
+template <int P, bool BF16, bool FULL>
+__device__ __forceinline__ void load_row(const void* z, int64_t t, int E, Row<P, BF16>& r) {
+  constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;     // -inf past E
   const int64_t at = t * E;
-  if ((E & 1) == 0) {
 #pragma unroll
-    for (int i = 0; i < P; i += 2) {
-      const int e = expert_of(i);
-      v[i] = v[i + 1] = -INFINITY;
-      if (e < E) {
-        if constexpr (BF16) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(
-              reinterpret_cast<const uint16_t*>(z) + at + e);
-          v[i] = bf16_lo(w);
-          v[i + 1] = bf16_hi(w);
-        } else {
-          const float2 w = *reinterpret_cast<const float2*>(
-              reinterpret_cast<const float*>(z) + at + e);
-          v[i] = w.x;
-          v[i + 1] = w.y;
+  for (int i = 0; i < P; i += 2) {
+    const int e = expert_of(i);
+    if constexpr (BF16) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(z) + at;
+      if (FULL || (E & 1) == 0) {
+        r.w[i / 2] = kNone;
+        if (FULL || e < E) r.w[i / 2] = *reinterpret_cast<const uint32_t*>(p + e);
+      } else {
+        uint32_t lo = 0xff80u, hi = 0xff80u;
+        if (e < E) lo = p[e];
+        if (e + 1 < E) hi = p[e + 1];
+        r.w[i / 2] = lo | (hi << 16);
+      }
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(z) + at;
+      if (FULL || (E & 1) == 0) {
+        r.w[i] = r.w[i + 1] = kNone;
+        if (FULL || e < E) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p + e);
+          r.w[i] = v.x;
+          r.w[i + 1] = v.y;
         }
+      } else {
+        r.w[i] = e < E ? p[e] : kNone;
+        r.w[i + 1] = e + 1 < E ? p[e + 1] : kNone;
       }
     }
-  } else {
+  }
+}
+
+template <int P, bool BF16>
+__device__ __forceinline__ void unpack_row(const Row<P, BF16>& r, float (&v)[P]) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = expert_of(i);
-      v[i] = e < E ? logit_at<BF16>(z, at + e) : -INFINITY;
-    }
+  for (int i = 0; i < P; ++i) {
+    if constexpr (BF16) v[i] = (i & 1) ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+    else v[i] = __uint_as_float(r.w[i]);
   }
 }
 
@@ -89,10 +116,32 @@ __device__ __forceinline__ int order_key(float f) {
   return f != f ? kKeyNone + 1 : b ^ ((b >> 31) & 0x7fffffff);
 }
 
-__device__ __forceinline__ float wave_max_f(float v) {        // NaN is passed over
-  const int k = wave_max(v != v ? kKeyNone : order_key(v));
-  if (k == kKeyNone) return -INFINITY;
+__device__ __forceinline__ float key_value(int k) {
   return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// Largest of the 64 lanes' values; NaN is passed over, -inf if there is no other.
+__device__ __forceinline__ float wave_max_f(float v) {
+  constexpr int lo = (int)0xff800000u;                      // -inf
+#define MOONEP_MAXF(ctrl, rows) \
+  v = fmaxf(v, __int_as_float(MOONEP_DPP(lo, __float_as_int(v), ctrl, rows)))
+  MOONEP_MAXF(0x111, 0xf);
+  MOONEP_MAXF(0x112, 0xf);
+  MOONEP_MAXF(0x114, 0xf);
+  MOONEP_MAXF(0x118, 0xf);
+  MOONEP_MAXF(0x142, 0xa);
+  MOONEP_MAXF(0x143, 0xc);
+#undef MOONEP_MAXF
+  v = __int_as_float(wave_bcast(__float_as_int(v), kWave - 1));
+  return v != v ? -INFINITY : v;
+}
+
+template <int P>
+__device__ __forceinline__ float lane_max(const float (&v)[P]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < P; ++i) m = fmaxf(m, v[i]);
+  return m;
 }
 
 __device__ __forceinline__ double wave_sum_d(double v) {
@@ -100,45 +149,87 @@ __device__ __forceinline__ double wave_sum_d(double v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) {
-  const float t = __expf(-fabsf(z));
-  const float r = __builtin_amdgcn_rcpf(1.f + t);
-  return z != z ? z : z >= 0.f ? r : t * r;
+__device__ __forceinline__ double lane_bcast_d(double v, int l) {
+  const int64_t b = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)wave_bcast((int)b, l);
+  const uint32_t hi = (uint32_t)wave_bcast((int)(b >> 32), l);
+  return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
 }
 
-// 1 - sigmoid(z) without cancellation.
-__device__ __forceinline__ float co_sigmoid_f(float z) { return sigmoid_f(-z); }
+__device__ __forceinline__ float exp_f(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+
+// sigmoid(z) and 1 - sigmoid(z), neither by cancellation; NaN stays NaN.
+__device__ __forceinline__ float sigmoid_f(float z, float& co) {
+  const float t = exp_f(-fabsf(z));
+  const float r = __builtin_amdgcn_rcpf(1.f + t), q = t * r;
+  co = z >= 0.f ? q : r;
+  return z >= 0.f ? r : q;
+}
+
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float co;
+  return sigmoid_f(z, co);
+}
 
 // Below this logit a sigmoid is e^z to fp32's last bit, and ratios of scores
 // are taken from e^(z - max) so that they survive the scores' underflow.
 constexpr float kDeep = -60.f;
 
-// Unnormalised p of a row: s (or its multiple) in v, and the factor 1 / sum.
-// A row whose every logit is -inf has p = 0.
-template <int P>
-__device__ __forceinline__ float row_shares(const float (&z)[P], float (&v)[P], int score,
-                                            float m) {
-  const bool soft = score == MOE_SCORE_SOFTMAX || m < kDeep;
+// Sums of exponentials in this range are taken as they are: the largest logit
+// is then between -15 and 13, so nothing overflows or underflows, and the
+// exponentials' errors are those of arguments of at most 15.  Other sums
+// (far logits, a masked row's 0, NaN) are taken again from z - max.
+constexpr float kPlainLo = 0x1p-10f, kPlainHi = 0x1p18f;
+// The same for sums of sigmoids: none of their terms that count has underflowed.
+constexpr float kSigmoidLo = 0x1p-60f;
+
+__device__ __forceinline__ float recip(float sum) {          // 0 for an empty sum
+  return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
+}
+
+// Unnormalised shares p of a row in v (co: 1 - s for sigmoids) and their
+// factor.  The scores of a softmax are e^(z - shift) times that factor.  A row
+// whose every logit is -inf has p = 0.
+template <int P, bool CO>
+__device__ __forceinline__ float row_shares(const float (&z)[P], float (&v)[P], float (&co)[P],
+                                            bool soft, float& shift) {
   float sum = 0.f;
+  shift = 0.f;
   if (soft) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      v[i] = m == -INFINITY && !(z[i] != z[i]) ? 0.f : __expf(z[i] - m);
+      v[i] = exp_f(z[i]);
       sum += v[i];
     }
+    sum = wave_sum_f(sum);
+    if (sum >= kPlainLo && sum <= kPlainHi) return recip(sum);
   } else {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      v[i] = sigmoid_f(z[i]);
+      float c;
+      v[i] = sigmoid_f(z[i], c);
+      if constexpr (CO) co[i] = c;
       sum += v[i];
     }
+    sum = wave_sum_f(sum);
+    if (sum >= kSigmoidLo) return recip(sum);
   }
-  sum = wave_sum_f(sum);
-  return sum == 0.f ? 0.f : 1.f / sum;
+  const float m = wave_max_f(lane_max<P>(z));
+  if (!soft && !(m < kDeep)) return recip(sum);              // NaN, for one
+  sum = 0.f;
+  if (m > -INFINITY) shift = m;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    v[i] = exp_f(z[i] - shift);
+    sum += v[i];
+  }
+  return recip(wave_sum_f(sum));
 }
 
 // The K largest keys in order, equal ones in ascending expert; lane k returns
-// the k-th id.  key is consumed.
+// the k-th id.  key is consumed.  Any keys: K rounds of a maximum of the wave.
 template <int P>
 __device__ __forceinline__ int take_top(int (&key)[P], int K) {
   const int lane = lane_id();
@@ -167,7 +258,91 @@ __device__ __forceinline__ int take_top(int (&key)[P], int K) {
   return mine;
 }
 
-// Scores s + bias of one expert in float64.
+// A bound t such that the K largest keys are among those >= t, and few others
+// are.  `top` is the lane's largest key, m the row's.  The K-th largest of the
+// 64 lanes' largest keys is such a bound; it is searched for on the scalar
+// unit, one comparison of the wave a step, first by doubling the distance to m
+// and then by halving the interval, until at most K + K/8 + 1 lanes reach it.
+// -inf where there is none above it (fewer than K lanes have a finite key).
+__device__ __forceinline__ float key_bound(float top, float m, int K) {
+  const int most = K + (K >> 3) + 1;
+  const int low = order_key(-INFINITY);
+  int hi = __builtin_amdgcn_readfirstlane(order_key(m)), lo = hi, n = 0;
+  for (int d = 1 << 21;; d <<= 1) {
+    if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
+    lo -= d;
+    n = (int)__popcll(__ballot(top >= key_value(lo)));
+    if (n >= K) break;
+    hi = lo;
+  }
+  while (n > most && hi - lo > 1) {
+    const int mid = lo + ((hi - lo) >> 1);
+    const int c = (int)__popcll(__ballot(top >= key_value(mid)));
+    if (c >= K) {
+      lo = mid;
+      n = c;
+    } else {
+      hi = mid;
+    }
+  }
+  return key_value(lo);
+}
+
+// Inserts every key >= t (at most 64 of them, none NaN) into a list that lies
+// sorted across the lanes: lane k gets the k-th key and its expert, equal keys
+// in ascending expert.
+template <int P>
+__device__ __forceinline__ void insert_all(const float (&key)[P], float t, float& mykey,
+                                           int& mine) {
+  float lk = -INFINITY;
+  int li = 0x7fffffff;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    uint64_t left = __ballot(key[i] >= t);
+    while (left) {
+      const int l = __ffsll((unsigned long long)left) - 1;
+      left &= left - 1;
+      const float v = __int_as_float(wave_bcast(__float_as_int(key[i]), l));
+      const int id = ((i >> 1) << 7) + 2 * l + (i & 1);
+      uint64_t before = __ballot(lk > v);
+      const uint64_t equal = __ballot(lk == v);
+      if (equal) before |= __ballot(lk == v && li < id);
+      const int pos = (int)__popcll(before);
+      const int uk = MOONEP_DPP(0, __float_as_int(lk), 0x138, 0xf);   // wave_shr:1
+      const int ui = MOONEP_DPP(0, li, 0x138, 0xf);
+      const bool stay = lane_id() < pos, here = lane_id() == pos;
+      lk = stay ? lk : here ? v : __int_as_float(uk);
+      li = stay ? li : here ? id : ui;
+    }
+  }
+  mykey = lk;
+  mine = li;
+}
+
+template <int P>
+__device__ __forceinline__ int reaching(const float (&key)[P], float t) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) n += (int)__popcll(__ballot(key[i] >= t));
+  return n;
+}
+
+// take_top through key_bound and insert_all.  False, and nothing done, where a
+// key is NaN or more keys than the list holds reach the bound.
+template <int P>
+__device__ __forceinline__ bool insert_top(const float (&key)[P], float top, float m, int K,
+                                           float& mykey, int& mine) {
+  uint64_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < P; i += 2) bad |= __ballot(__builtin_isunordered(key[i], key[i + 1]));
+  if (bad) return false;
+  const float t = key_bound(top, m, K);
+  if (t == -INFINITY || reaching<P>(key, t) > kWave) return false;
+  insert_all<P>(key, t, mykey, mine);
+  return true;
+}
+
+// Score plus bias of one expert in float64.
 template <bool BF16>
 __device__ __forceinline__ double key64(const RouterArgs& a, int64_t at, int e, double m,
                                         double sum) {
@@ -178,32 +353,34 @@ __device__ __forceinline__ double key64(const RouterArgs& a, int64_t at, int e, 
   return s + (double)a.bias[e];
 }
 
-// take_top on the float64 scores plus bias, for a row whose fp32 ones are too
-// near each other to order.  Rare, so nothing is kept in registers between
+// Sum of a row's e^(z - m) in float64.
+template <int P, bool BF16>
+__device__ double sum64(const RouterArgs& a, int64_t at, double m) {
+  double sum = 0.0;
+  for (int i = 0; i < P; ++i) {
+    const int e = expert_of(i);
+    if (e < a.E) {
+      const double z = (double)logit_at<BF16>(a.logits, at + e);
+      if (!(m == -INFINITY && z == z)) sum += exp(z - m);
+    }
+  }
+  return wave_sum_d(sum);
+}
+
+// take_top on the float64 scores plus bias: the K largest, equal ones in
+// ascending expert, NaN last.  For rows that nothing else orders (NaN, more
+// than 64 keys near each other), so nothing is kept in registers between
 // rounds: the scores are computed anew.
 template <int P, bool BF16>
-__device__ int take_top64(const RouterArgs& a, int64_t t, float mf) {
+__device__ int take_top64(const RouterArgs& a, int64_t at, double m, double sum) {
   const int lane = lane_id();
-  const int64_t at = t * a.E;
-  const double m = (double)mf;
-  double sum = 1.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    sum = 0.0;
-    for (int i = 0; i < P; ++i) {
-      const int e = expert_of(i);
-      if (e < a.E) {
-        const double z = (double)logit_at<BF16>(a.logits, at + e);
-        if (!(m == -INFINITY && z == z)) sum += exp(z - m);
-      }
-    }
-    sum = wave_sum_d(sum);
-  }
   uint32_t taken = 0;                            // P <= 32 bits
   int mine = 0;
   for (int k = 0; k < a.K; ++k) {
-    // rank of a candidate: numbers by value, then NaN, then nothing
+    // class of a candidate: 2 a number, 1 NaN, 0 none
     double best = 0.0;
     int cls = 0, id = 0x7fffffff, bi = 0;
+#pragma unroll 1
     for (int i = 0; i < P; ++i) {
       const int e = expert_of(i);
       if (e >= a.E || (taken >> i & 1)) continue;
@@ -216,7 +393,7 @@ __device__ int take_top64(const RouterArgs& a, int64_t t, float mf) {
         bi = i;
       }
     }
-    const int mybi = bi, myid = id;
+    const int myid = id;
     for (int o = 32; o > 0; o >>= 1) {
       const double od = __shfl_xor(best, o, kWave);
       const int oc = __shfl_xor(cls, o, kWave), oi = __shfl_xor(id, o, kWave);
@@ -227,75 +404,102 @@ __device__ int take_top64(const RouterArgs& a, int64_t t, float mf) {
         id = oi;
       }
     }
-    if (id == myid && cls > 0) taken |= 1u << mybi;
+    if (id == myid && cls > 0) taken |= 1u << bi;
     if (lane == k) mine = id;
   }
   return mine;
 }
 
-// Lane k < K: the k-th chosen expert of token t.  m is the row's largest
-// logit.
+// Lane k < K: the k-th expert by score plus bias, and its logit zk.
 //
-// With a bias the order is that of float64 s + bias.  fp32 keys order all rows
-// but those where two neighbours among the K + 1 largest are nearer than the
-// keys' errors: s from v_exp_f32 and v_rcp_f32 (1 ulp each) is off by
-//   sigmoid  s (1 - s) |z| 2^-24 + 2.5 ulp  <=  1.4e-8 + 2.5 * 2^-23 s,
-//   softmax  s (|z - m| 2^-24 + the sum's) <= 8e-6 s  (s > 0 needs |z - m| < 104),
-// and the sum with the bias by 2^-24 |key|.  Such rows are taken again in
-// float64; equal logits with equal biases need no second look.
+// The order is that of float64 scores plus bias; fp32 keys give it wherever
+// neighbours among the K + 1 largest keys are further apart than two keys'
+// errors.  With h = 2^-24 a key is off by
+//   sigmoid  s (1 - s) |z| 2.2 h + 2.5 ulp of s  <=  1.4e-8 + 3e-7,
+//   softmax  s (|z - shift| 2.2 h + the sum's relative error), where
+//            s |z - max| <= 0.37 p_max and the sum's error is at most
+//            (2.2 ln E + 48 + 33) h:  <= 8e-6 p_max,
+// and by h |key| from the addition.  Other rows list every key that may be
+// among the K largest, at most 64, and order those in float64, a lane each.
 template <int P, bool BF16>
-__device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
-                                      const float (&v)[P], float inv, float m) {
-  int key[P];
-  if (!a.bias) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
-    return take_top<P>(key, a.K);
-  }
+__device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, const float (&z)[P],
+                                             const float (&s)[P], const float (&bias)[P],
+                                             float inv, float shift, float& zk) {
+  const int lane = lane_id();
+  const int64_t at = t * a.E;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
   const int n = a.K < a.E ? a.K + 1 : a.K;
-  if (n <= kWave) {
+  float key[P], lk;
+  int id = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = expert_of(i);
-      key[i] = e < a.E ? order_key((soft ? v[i] * inv : sigmoid_f(z[i])) + a.bias[e]) : kKeyNone;
+  for (int i = 0; i < P; ++i) key[i] = fmaf(s[i], inv, bias[i]);
+  const float top = lane_max<P>(key);
+  bool listed = n <= kWave && insert_top<P>(key, top, wave_max_f(top), n, lk, id);
+  float m = 0.f;                                         // only softmax looks at it
+  if (soft) m = wave_max_f(lane_max<P>(z));
+  if (listed) {
+    const float err = soft ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
+    const float ko = __shfl_down(lk, 1, kWave);
+    const bool apart = lk - ko > 2.f * err + 1.2e-7f * (fabsf(lk) + fabsf(ko));
+    if (!__all(lane >= n - 1 || apart)) {
+      const float last = __int_as_float(wave_bcast(__float_as_int(lk), a.K - 1));
+      const float reach = last - (2.f * err + 2.4e-7f * fabsf(last) + 1e-12f);
+      const int cnt = reaching<P>(key, reach);
+      listed = reach > -INFINITY && cnt <= kWave;
+      if (listed) {
+        insert_all<P>(key, reach, lk, id);
+        const double sum = soft ? sum64<P, BF16>(a, at, (double)m) : 1.0;
+        const double mine =
+            lane < cnt ? key64<BF16>(a, at, id, (double)m, sum) : 0.0;
+        int rank = 0;
+        for (int j = 0; j < cnt; ++j) {
+          const double kj = lane_bcast_d(mine, j);
+          const int ij = wave_bcast(id, j);
+          rank += kj > mine || (kj == mine && ij < id) ? 1 : 0;
+        }
+        id = __builtin_amdgcn_ds_permute(4 * (lane < cnt ? rank : lane), id);
+      }
     }
-    const int id = take_top<P>(key, n);
-    const int lane = lane_id();
-    const int at = lane < n ? id : 0;
-    const float zi = logit_at<BF16>(a.logits, t * a.E + at), bi = a.bias[at];
-    const float s = soft ? (m == -INFINITY ? 0.f : __expf(zi - m) * inv) : sigmoid_f(zi);
-    const float k = s + bi;
-    const float zo = __shfl_down(zi, 1, kWave), bo = __shfl_down(bi, 1, kWave);
-    const float so = __shfl_down(s, 1, kWave), ko = __shfl_down(k, 1, kWave);
-    const float tol = (soft ? 8e-6f * (s + so) : 4e-7f * (s + so) + 4e-8f) +
-                      1.2e-7f * (fabsf(k) + fabsf(ko));
-    const bool same = zi == zo && bi == bo;
-    const bool clear = same || k - ko > tol;             // NaN is never clear
-    if (__all(lane >= n - 1 || clear)) return id;
   }
-  return take_top64<P, BF16>(a, t, m);
+  if (!listed)
+    id = take_top64<P, BF16>(a, at, (double)m, soft ? sum64<P, BF16>(a, at, (double)m) : 1.0);
+  zk = logit_at<BF16>(a.logits, at + (lane < a.K ? id : 0));
+  return id;
 }
 
-// Lane k < K: score of the chosen logit zk relative to `total`, such that the
-// gate is scale * w.
-__device__ __forceinline__ float gate_share(float zk, bool on, int score, bool renorm, float m,
+// Lane k < K: the k-th expert by logit, and its logit zk.
+template <int P, bool BF16>
+__device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
+                                      float& zk) {
+  int id = 0;
+  const float top = lane_max<P>(z);
+  if (insert_top<P>(z, top, wave_max_f(top), a.K, zk, id)) return id;
+  int key[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
+  id = take_top<P>(key, a.K);
+  zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
+  return id;
+}
+
+// Lane k < K (`on`): the gate of the chosen logit zk, over scale.
+__device__ __forceinline__ float gate_share(float zk, bool on, bool soft, bool renorm, float shift,
                                             float inv) {
   if (!renorm) {
     if (!on) return 0.f;
-    if (score == MOE_SCORE_SIGMOID) return sigmoid_f(zk);
-    return m == -INFINITY && zk == zk ? 0.f : __expf(zk - m) * inv;
+    return soft ? exp_f(zk - shift) * inv : sigmoid_f(zk);
   }
-  const float mk = wave_max_f(on ? zk : -INFINITY);
-  float s = 0.f;
-  if (on) {
-    if (score == MOE_SCORE_SOFTMAX || mk < kDeep)
-      s = mk == -INFINITY && zk == zk ? 0.f : __expf(zk - mk);
-    else
-      s = sigmoid_f(zk);
+  float s = on ? soft ? exp_f(zk) : sigmoid_f(zk) : 0.f;
+  float sum = wave_sum_f(s);
+  const bool plain = soft ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo;
+  if (!plain) {
+    const float mk = wave_max_f(on ? zk : -INFINITY);
+    if (soft || mk < kDeep) {
+      s = on ? exp_f(mk > -INFINITY ? zk - mk : zk) : 0.f;
+      sum = wave_sum_f(s);
+    }
   }
-  const float sum = wave_sum_f(s);
-  return sum == 0.f ? 0.f : s / sum;
+  return s * recip(sum);
 }
 
 // The sequence that holds token t (the last one with cu[s] <= t), or -1, and
@@ -321,19 +525,25 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 
 // ---------------------------------------------------------------------------
 // Forward.  A workgroup owns `chunk` consecutive tokens, its waves take them in
-// turn.  Where the loss is wanted, each wave keeps the sums of p in registers
-// and the workgroup the counts in LDS; both go to row (workgroup + sequence)
-// of the workspace when the sequence or the chunk ends.  Along the tokens
-// either number grows, so no two pieces share a row.
+// turn, each loading its next row before it works on the present one.  Where
+// the loss is wanted, each wave keeps the sums of p in registers and the
+// workgroup the counts in LDS; both go to row (workgroup + sequence) of the
+// workspace when the sequence or the chunk ends.  Along the tokens either
+// number grows, so no two pieces share a row.
 // ---------------------------------------------------------------------------
-template <int P, bool BF16, bool SELECT, bool STATS>
+template <int P, bool BF16, bool FULL, bool SELECT, bool BIAS, bool STATS>
 __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
   extern __shared__ float lds[];                  // [waves][E] sums, [E] counts
-  const int lane = lane_id(), wv = threadIdx.x / kWave;
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
+  const bool soft = a.score == MOE_SCORE_SOFTMAX;
   int* cnt = reinterpret_cast<int*>(lds + kRtWaves * E);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-  float acc[P];
+  float acc[P], bias[P];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) bias[i] = expert_of(i) < E ? a.bias[expert_of(i)] : -INFINITY;
+  }
   for (int lo = t0; lo < t1;) {
     int hi = t1, seq = -1;
     if constexpr (STATS) {
@@ -345,36 +555,45 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
       __syncthreads();
     }
     if (SELECT || seq >= 0) {
+      Row<P, BF16> next;
+      if (lo + wv < hi) load_row<P, BF16, FULL>(a.logits, lo + wv, E, next);
       for (int t = lo + wv; t < hi; t += kRtWaves) {
-        float z[P], v[P];
-        load_row<P, BF16>(a.logits, t, E, z);
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < P; ++i) m = fmaxf(m, z[i]);
-        m = wave_max_f(m);
-        float inv = 0.f;
-        const bool shares = STATS || (SELECT && a.score == MOE_SCORE_SOFTMAX &&
-                                      (a.bias || !a.renorm));
-        if (shares) inv = row_shares<P>(z, v, a.score, m);
+        float z[P], v[P], co[P];
+        unpack_row<P, BF16>(next, z);
+        if (t + kRtWaves < hi) load_row<P, BF16, FULL>(a.logits, t + kRtWaves, E, next);
         int id = -1;
+        if constexpr (!SELECT) {
+          if (lane < K) id = a.ids[int64_t(t) * K + lane];
+        }
+        float inv = 1.f, shift = 0.f;
+        if (STATS || (SELECT && soft && (BIAS || !a.renorm)))
+          inv = row_shares<P, false>(z, v, co, soft, shift);
+        if constexpr (STATS) {
+          if (seq >= 0) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+          }
+        }
         if constexpr (SELECT) {
-          id = choose<P, BF16>(a, t, z, v, inv, m);
+          float zk;
+          if constexpr (BIAS) {
+            if (!soft && (!STATS || shift != 0.f)) {      // v holds no sigmoids
+#pragma unroll
+              for (int i = 0; i < P; ++i) v[i] = sigmoid_f(z[i]);
+            }
+            id = choose_biased<P, BF16>(a, t, z, v, bias, soft ? inv : 1.f, shift, zk);
+          } else {
+            id = choose<P, BF16>(a, t, z, zk);
+          }
           const bool on = lane < K;
-          const float zk = on ? logit_at<BF16>(a.logits, int64_t(t) * E + id) : 0.f;
-          const float w = gate_share(zk, on, a.score, a.renorm, m, inv);
+          const float w = gate_share(zk, on, soft, a.renorm, shift, inv);
           if (on) {
             a.ids[int64_t(t) * K + lane] = id;
             a.gates[int64_t(t) * K + lane] = a.scale * w;
           }
-        } else {
-          if (lane < K) id = a.ids[int64_t(t) * K + lane];
         }
         if constexpr (STATS) {
-          if (seq >= 0) {
-            if (lane < K && (unsigned)id < (unsigned)E) atomicAdd(&cnt[id], 1);
-#pragma unroll
-            for (int i = 0; i < P; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-          }
+          if (seq >= 0 && lane < K && (unsigned)id < (unsigned)E) atomicAdd(&cnt[id], 1);
         }
       }
     }
@@ -383,7 +602,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int e = expert_of(i);
-          if (e < E) lds[wv * E + e] = acc[i];
+          if (FULL || e < E) lds[wv * E + e] = acc[i];
         }
       }
       __syncthreads();
@@ -403,52 +622,71 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
   }
 }
 
-// Joins a sequence's rows, in the order of its chunks, into counts, P and the
-// loss.  One workgroup per sequence.
-constexpr int kFinThreads = 1024;
+// Joins a sequence's rows, in the order of its chunks, into counts and P, and
+// the loss where one workgroup has all experts.  A workgroup takes `ns` slices
+// of 64 experts of one sequence; its 16 waves are 16 / ns groups that take the
+// rows in turn.
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinWaves = kJoinThreads / kWave;
 
-__global__ __launch_bounds__(kFinThreads) void k_router_finish(RouterArgs a, int chunks,
+__global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int chunks, int ns,
                                                               int32_t* counts, float* prob,
                                                               float* loss) {
-  constexpr int W = kFinThreads / kWave;
-  __shared__ double s_p[W][kWave];
-  __shared__ int s_c[W][kWave];
+  __shared__ double s_p[kJoinWaves][kWave];
+  __shared__ int s_c[kJoinWaves][kWave];
   const int seq = blockIdx.x, lane = lane_id(), wv = threadIdx.x / kWave;
+  const int groups = kJoinWaves / ns, slice = wv % ns, group = wv / ns;
   const int lo = a.cu ? max(0, min(a.cu[seq], a.T)) : 0;
   const int hi = a.cu ? max(lo, min(a.cu[seq + 1], a.T)) : a.T;
   const int c0 = hi > lo ? lo / a.chunk : 0, c1 = hi > lo ? min((hi - 1) / a.chunk + 1, chunks) : 0;
-  const double len = hi > lo ? (double)(hi - lo) : 1.0;
+  const int e = (blockIdx.y * ns + slice) * kWave + lane;
+  double p = 0.0;
+  int c = 0;
+  if (e < a.E && group < groups) {
+#pragma unroll 8
+    for (int r = c0 + group; r < c1; r += groups) {
+      const int64_t at = int64_t(r + seq) * a.E + e;
+      p += (double)a.part_p[at];
+      c += a.part_c[at];
+    }
+  }
+  s_p[wv][lane] = p;
+  s_c[wv][lane] = c;
+  __syncthreads();
+  double f = 0.0;
+  if (group == 0 && e < a.E) {
+    for (int g = 1; g < groups; ++g) {
+      p += s_p[g * ns + slice][lane];
+      c += s_c[g * ns + slice][lane];
+    }
+    const float mean = hi > lo ? (float)(p / (double)(hi - lo)) : 0.f;
+    counts[int64_t(seq) * a.E + e] = c;
+    prob[int64_t(seq) * a.E + e] = mean;
+    f = (double)c * (double)mean;
+  }
+  if (gridDim.y > 1) return;                      // k_router_loss follows
+  __syncthreads();
+  f = wave_sum_d(f);
+  if (lane == 0) s_p[wv][0] = f;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < ns; ++w) f += s_p[w][0];
+    loss[seq] = hi > lo ? (float)(f * a.E / ((double)a.K * (hi - lo))) : 0.f;
+  }
+}
+
+// The loss of a sequence from its counts and P: one wave.
+__global__ __launch_bounds__(kWave) void k_router_loss(RouterArgs a, const int32_t* counts,
+                                                       const float* prob, float* loss) {
+  const int seq = blockIdx.x;
+  const int lo = a.cu ? max(0, min(a.cu[seq], a.T)) : 0;
+  const int hi = a.cu ? max(lo, min(a.cu[seq + 1], a.T)) : a.T;
   double total = 0.0;
-  for (int e0 = 0; e0 < a.E; e0 += kWave) {
-    const int e = e0 + lane;
-    double p = 0.0;
-    int c = 0;
-    if (e < a.E) {
-      for (int r = c0 + wv; r < c1; r += W) {
-        const int64_t at = int64_t(r + seq) * a.E + e;
-        p += (double)a.part_p[at];
-        c += a.part_c[at];
-      }
-    }
-    s_p[wv][lane] = p;
-    s_c[wv][lane] = c;
-    __syncthreads();
-    if (wv == 0 && e < a.E) {
-      for (int w = 1; w < W; ++w) {
-        p += s_p[w][lane];
-        c += s_c[w][lane];
-      }
-      const double mean = p / len;
-      counts[int64_t(seq) * a.E + e] = c;
-      prob[int64_t(seq) * a.E + e] = (float)mean;
-      total += (double)a.E * c / (a.K * len) * mean;
-    }
-    __syncthreads();
-  }
-  if (wv == 0) {
-    total = wave_sum_d(total);
-    if (lane == 0) loss[seq] = (float)total;
-  }
+  for (int e = lane_id(); e < a.E; e += kWave)
+    total += (double)counts[int64_t(seq) * a.E + e] * (double)prob[int64_t(seq) * a.E + e];
+  total = wave_sum_d(total);
+  if (lane_id() == 0)
+    loss[seq] = hi > lo ? (float)(total * a.E / ((double)a.K * (hi - lo))) : 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -462,24 +700,57 @@ __global__ __launch_bounds__(kFinThreads) void k_router_finish(RouterArgs a, int
 //   renormalised               scale w_k (dg_k - sum dg w) (1 - s_k for sigmoid),
 //   sigmoid, not renormalised  scale dg_k s_k (1 - s_k).
 // These K values reach the lanes that hold their experts through an LDS row.
+// A gradient of renormalised gates alone reads only the K chosen logits.
 // ---------------------------------------------------------------------------
-template <int P, bool BF16>
+template <int P, bool BF16, bool FULL>
 __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
-  extern __shared__ float lds[];                  // [waves][E]
-  const int lane = lane_id(), wv = threadIdx.x / kWave;
+  extern __shared__ float lds[];                  // [waves][64 P]
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
-  float* row = lds + wv * E;
+  float* row = lds + wv * (64 * P);
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
   const bool balance = a.dloss != nullptr, gates = a.dgates != nullptr;
   const bool into_u = soft && gates && !a.renorm;         // the gates' part goes through p
-  for (int e = lane; e < E; e += kWave) row[e] = 0.f;
+  if (gates) {
+#pragma unroll
+    for (int i = 0; i < P; i += 2) *reinterpret_cast<float2*>(row + expert_of(i)) = float2{0, 0};
+  }
   const int64_t w0 = (int64_t(blockIdx.x) * kRtWaves + wv) * a.chunk;
   const int t0 = (int)min<int64_t>(w0, a.T), t1 = (int)min<int64_t>(w0 + a.chunk, a.T);
+  if (t0 >= t1) return;
+  const bool rows = balance || into_u;
+  Row<P, BF16> next;
+  int next_id = -1;
+  float next_dg = 0.f;
+  if (rows) load_row<P, BF16, FULL>(a.logits, t0, E, next);
+  if (gates && lane < K) {
+    next_id = a.ids[int64_t(t0) * K + lane];
+    next_dg = a.dgates[int64_t(t0) * K + lane];
+  }
   int end = t0, seq = -1;
   float u[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) u[i] = 0.f;
   for (int t = t0; t < t1; ++t) {
+    float v[P], co[P], dz[P];
+    float shift = 0.f, inv = 1.f;
+    if (rows) {
+      float z[P];
+      unpack_row<P, BF16>(next, z);
+      if (t + 1 < t1) load_row<P, BF16, FULL>(a.logits, t + 1, E, next);
+      inv = row_shares<P, true>(z, v, co, soft, shift);
+      if (!soft && shift != 0.f) {                // deep row: v is not s, but 1 - s is 1
+#pragma unroll
+        for (int i = 0; i < P; ++i) co[i] = 1.f;
+      }
+    }
+    const int id = next_id;
+    const bool on = (unsigned)id < (unsigned)E;
+    float dg = on ? a.scale * next_dg : 0.f;
+    if (gates && lane < K && t + 1 < t1) {
+      next_id = a.ids[int64_t(t + 1) * K + lane];
+      next_dg = a.dgates[int64_t(t + 1) * K + lane];
+    }
     if (balance && t >= end) {
       seq = sequence_of(a, t, end);
       float c0 = 0.f;
@@ -494,81 +765,82 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
         u[i] = seq >= 0 && e < E ? c0 * (float)a.counts[int64_t(seq) * E + e] : 0.f;
       }
     }
-    const bool bal = balance && seq >= 0;
-    float z[P], v[P], dz[P];
-    float m = -INFINITY, inv = 0.f;
-    if (bal || into_u) {
-      load_row<P, BF16>(a.logits, t, E, z);
-#pragma unroll
-      for (int i = 0; i < P; ++i) m = fmaxf(m, z[i]);
-      m = wave_max_f(m);
-      inv = row_shares<P>(z, v, a.score, m);
-    }
-    int id = -1;
     if (gates) {
-      if (lane < K) id = a.ids[int64_t(t) * K + lane];
-      const bool on = (unsigned)id < (unsigned)E;
-      const float zk = on ? logit_at<BF16>(a.logits, int64_t(t) * E + id) : 0.f;
-      const float dg = on ? a.scale * a.dgates[int64_t(t) * K + lane] : 0.f;
-      float val = dg;
       if (!into_u) {
-        const float w = gate_share(zk, on, a.score, a.renorm, m, inv);
-        const float mean = a.renorm ? wave_sum_f(dg * w) : 0.f;
-        val = w * (dg - mean);
-        if (!soft) val *= co_sigmoid_f(zk);
+        const float zk = on ? logit_at<BF16>(a.logits, int64_t(t) * E + id) : 0.f;
+        const float w = gate_share(zk, on, soft, a.renorm, shift, inv);
+        dg = w * (dg - (a.renorm ? wave_sum_f(dg * w) : 0.f));
+        if (!soft) {
+          float c;
+          sigmoid_f(zk, c);
+          dg *= c;
+        }
       }
-      if (on) atomicAdd(&row[id], val);
+      if (on) atomicAdd(&row[id], dg);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
 #pragma unroll
-    for (int i = 0; i < P; ++i) dz[i] = gates && expert_of(i) < E ? row[expert_of(i)] : 0.f;
-    if (gates) {
+      for (int i = 0; i < P; i += 2) {
+        const float2 g = *reinterpret_cast<const float2*>(row + expert_of(i));
+        dz[i] = g.x;
+        dz[i + 1] = g.y;
+      }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if ((unsigned)id < (unsigned)E) row[id] = 0.f;
+      if (on) row[id] = 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dz[i] = 0.f;
     }
-    if (bal || into_u) {
+    if (into_u || (balance && seq >= 0)) {        // a row of no sequence may hold anything
       float mean = 0.f;
+      if (into_u) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        v[i] *= inv;
-        const float ui = (bal ? u[i] : 0.f) + (into_u ? dz[i] : 0.f);
-        mean = fmaf(ui, v[i], mean);
+        for (int i = 0; i < P; ++i) {
+          dz[i] += u[i];
+          mean = fmaf(dz[i], v[i], mean);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) mean = fmaf(u[i], v[i], mean);
       }
-      mean = wave_sum_f(mean);
+      mean = wave_sum_f(mean) * inv;
+      if (into_u) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float ui = (bal ? u[i] : 0.f) + (into_u ? dz[i] : 0.f);
-        const float g = v[i] * (ui - mean) * (soft ? 1.f : co_sigmoid_f(z[i]));
-        dz[i] = (into_u ? 0.f : dz[i]) + g;
+        for (int i = 0; i < P; ++i) dz[i] = v[i] * inv * (dz[i] - mean);
+      } else if (soft) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) dz[i] = fmaf(v[i] * inv, u[i] - mean, dz[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) dz[i] = fmaf(v[i] * inv * co[i], u[i] - mean, dz[i]);
       }
     }
     const int64_t at = int64_t(t) * E;
-    if ((E & 1) == 0) {
 #pragma unroll
-      for (int i = 0; i < P; i += 2) {
-        const int e = expert_of(i);
-        if (e < E) {
+    for (int i = 0; i < P; i += 2) {
+      const int e = expert_of(i);
+      if (FULL || (E & 1) == 0) {
+        if (FULL || e < E) {
           if constexpr (BF16)
             *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.dlogits) + at + e) =
-                pack_bf16x2(dz[i], dz[i + 1]);
+                cvt_bf16x2(dz[i], dz[i + 1]);
           else
             *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.dlogits) + at + e) =
                 float2{dz[i], dz[i + 1]};
         }
-      }
-    } else {
+      } else {
+        const uint32_t w = BF16 ? cvt_bf16x2(dz[i], dz[i + 1]) : 0u;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int e = expert_of(i);
-        if (e < E) {
-          if constexpr (BF16)
-            reinterpret_cast<uint16_t*>(a.dlogits)[at + e] = (uint16_t)f32_to_bf16(dz[i]);
-          else
-            reinterpret_cast<float*>(a.dlogits)[at + e] = dz[i];
+        for (int j = 0; j < 2; ++j) {
+          if (e + j < E) {
+            if constexpr (BF16)
+              reinterpret_cast<uint16_t*>(a.dlogits)[at + e + j] = (uint16_t)(w >> (16 * j));
+            else
+              reinterpret_cast<float*>(a.dlogits)[at + e + j] = dz[i + j];
+          }
         }
       }
     }
@@ -576,8 +848,14 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
 }
 
 // Tokens per workgroup and workgroups of a forward call that keeps sums.
-inline int stats_chunk(int T) { return T > 0 ? (T + kRtMaxChunks - 1) / kRtMaxChunks : 1; }
+inline int stats_chunk(int T) {
+  const int c = (T + kRtMaxChunks - 1) / kRtMaxChunks;
+  return c > 2 * kRtWaves ? c : 2 * kRtWaves;
+}
 inline int stats_chunks(int T) { return T > 0 ? (T + stats_chunk(T) - 1) / stats_chunk(T) : 0; }
+
+// Rows times slices of experts up to which one workgroup joins a sequence.
+constexpr int kJoinOne = 512;
 
 inline size_t part_rows(int T, int nseq) { return size_t(stats_chunks(T)) + size_t(nseq); }
 
@@ -592,21 +870,27 @@ inline int check_router(const moe_cfg* c, const moe_router_cfg* r) {
   return MOE_OK;
 }
 
-// Calls f with the registers per lane of a row of E experts and the type.
+// Calls f with the registers per lane of a row of E experts, the type, and
+// whether the row fills all lanes.
 template <typename F>
 inline int with_row(int E, bool bf16, F f) {
   const int p = 2 * ((E + 127) / 128);
-#define MOE_ROW(N)                                                       \
-  if (p <= N)                                                            \
-  return bf16 ? f(std::integral_constant<int, N>(), std::true_type())    \
-              : f(std::integral_constant<int, N>(), std::false_type())
-  MOE_ROW(2);
-  MOE_ROW(4);
-  MOE_ROW(6);
-  MOE_ROW(8);
-  MOE_ROW(14);
-  MOE_ROW(20);
-  MOE_ROW(32);
+#define MOE_ROW(N)                                                                      \
+  if (p <= N) {                                                                         \
+    constexpr std::integral_constant<int, N> n;                                         \
+    if (E == 64 * N)                                                                    \
+      return bf16 ? f(n, std::true_type(), std::true_type())                            \
+                  : f(n, std::false_type(), std::true_type());                          \
+    return bf16 ? f(n, std::true_type(), std::false_type())                             \
+                : f(n, std::false_type(), std::false_type());                           \
+  }
+  MOE_ROW(2)
+  MOE_ROW(4)
+  MOE_ROW(6)
+  MOE_ROW(8)
+  MOE_ROW(14)
+  MOE_ROW(20)
+  MOE_ROW(32)
 #undef MOE_ROW
   return MOE_ELIMIT;
 }
@@ -634,20 +918,30 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
   if (a.T > 0) {
     const int grid = stats ? chunks : (a.T + a.chunk - 1) / a.chunk;
     const size_t lds = stats ? size_t(kRtWaves + 1) * a.E * 4 : 0;
-    const int rc = with_row(a.E, r->logits_bf16, [&](auto p, auto b) {
+    const int rc = with_row(a.E, r->logits_bf16, [&](auto p, auto b, auto full) {
       constexpr int P = decltype(p)::value;
-      constexpr bool BF = decltype(b)::value;
+      constexpr bool BF = decltype(b)::value, FULL = decltype(full)::value;
       const dim3 g(grid), t(kRtThreads);
-      if (select && stats) hipLaunchKernelGGL((k_router<P, BF, true, true>), g, t, lds, stream, a);
-      else if (select) hipLaunchKernelGGL((k_router<P, BF, true, false>), g, t, lds, stream, a);
-      else hipLaunchKernelGGL((k_router<P, BF, false, true>), g, t, lds, stream, a);
+#define MOE_ROUTER(SEL, BIAS, STATS) \
+  hipLaunchKernelGGL((k_router<P, BF, FULL, SEL, BIAS, STATS>), g, t, lds, stream, a)
+      if (!select) MOE_ROUTER(false, false, true);
+      else if (stats && a.bias) MOE_ROUTER(true, true, true);
+      else if (stats) MOE_ROUTER(true, false, true);
+      else if (a.bias) MOE_ROUTER(true, true, false);
+      else MOE_ROUTER(true, false, false);
+#undef MOE_ROUTER
       return hip_status();
     });
     if (rc != MOE_OK) return rc;
   }
   if (stats) {
-    hipLaunchKernelGGL(k_router_finish, dim3(a.nseq), dim3(kFinThreads), 0, stream, a, chunks,
-                       counts, prob, loss);
+    const int slices = (a.E + kWave - 1) / kWave;
+    const bool one = slices <= kJoinWaves && chunks * slices <= kJoinOne;
+    hipLaunchKernelGGL(k_router_join, dim3(a.nseq, one ? 1 : slices), dim3(kJoinThreads), 0, stream,
+                       a, chunks, one ? slices : 1, counts, prob, loss);
+    if (!one && slices > 1)
+      hipLaunchKernelGGL(k_router_loss, dim3(a.nseq), dim3(kWave), 0, stream, a, counts, prob,
+                         loss);
     return hip_status();
   }
   return MOE_OK;
@@ -731,11 +1025,12 @@ extern "C" int moe_router_backward(const moe_cfg* cfg, const moe_router_cfg* rcf
   a.score = rcfg->score;
   a.renorm = rcfg->renormalize;
   a.scale = rcfg->scale;
-  a.chunk = a.T >= (1 << 15) ? 8 : 1;
+  a.chunk = std::max(1, std::min(8, a.T >> 13));
   const int per = kRtWaves * a.chunk;
-  const size_t lds = size_t(kRtWaves) * a.E * 4;
-  return with_row(a.E, rcfg->logits_bf16, [&](auto p, auto b) {
-    hipLaunchKernelGGL((k_router_bwd<decltype(p)::value, decltype(b)::value>),
+  return with_row(a.E, rcfg->logits_bf16, [&](auto p, auto b, auto full) {
+    constexpr int P = decltype(p)::value;
+    const size_t lds = dgates ? size_t(kRtWaves) * 64 * P * 4 : 0;
+    hipLaunchKernelGGL((k_router_bwd<P, decltype(b)::value, decltype(full)::value>),
                        dim3((a.T + per - 1) / per), dim3(kRtThreads), lds, stream, a);
     return hip_status();
   });

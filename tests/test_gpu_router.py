@@ -3,12 +3,14 @@
 Tolerances, from the arithmetic, with h = 2^-24 (half an fp32 step, relative):
 
 * a score's exponential: its argument x is rounded (|x| h), multiplied by
-  log2 e (|x| h again) and exponentiated (1 ulp = 2 h): (2 |x| + 2) h.  |x| is
-  at most X = the largest |z - max z| of the row among finite logits (sigmoid:
-  the largest |z|), counted up to 110, past which the score is 0 in fp32;
-* the sum over E experts: P <= 32 additions in a lane and 6 across lanes, and
-  the reciprocal and products that follow, 4 more: a share is off by
-  rel = (4 X + 2 + 32 + 6 + 8) h at most;
+  log2 e, itself rounded (0.2 h), (|x| h again) and exponentiated (1 ulp = 2 h):
+  (2.2 |x| + 2) h.  |x| is at most X = the largest |z - max z| of the row among
+  finite logits (sigmoid: the largest |z|), counted up to 110, past which the
+  score is 0 in fp32, and from 15 on: a softmax whose largest logit lies
+  between -15 and 13 is not shifted by it, which lengthens |x| by 15 at most;
+* the sum over E experts, whose terms are off by as much: P <= 32 additions in
+  a lane and 6 across lanes, and the reciprocal and products that follow, 4
+  more: a share is off by rel = (5 X + 2 + 32 + 6 + 8) h at most;
 * what fp32 cannot hold (scores below 2^-126) is 2^-126 absolute;
 * the sums over a sequence: one wave adds at most chunk / 4 tokens, then 4
   waves; the join is float64.  chunk = ceil(T / 1024);
@@ -72,11 +74,11 @@ def spread(z, score):
         x = np.nan_to_num(np.abs(f)).max(axis=1)
     else:
         x = np.where(np.isnan(f), -np.inf, f).max(axis=1) - np.where(np.isnan(f), np.inf, f).min(axis=1)
-    return np.clip(x, 0.0, 110.0)[:, None]
+    return np.clip(x, 15.0, 110.0)[:, None]
 
 
 def rel_of(z, score):
-    return (4 * spread(z, score) + 48) * h
+    return (5 * spread(z, score) + 48) * h
 
 
 def run_forward(c, rc, z, bias, cu, stats):
