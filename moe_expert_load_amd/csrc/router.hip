@@ -120,20 +120,17 @@ __device__ __forceinline__ float key_value(int k) {
   return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
-// Largest of the 64 lanes' values; NaN is passed over, -inf if there is no other.
+__device__ __forceinline__ uint64_t ballot(bool b) { return __builtin_amdgcn_ballot_w64(b); }
+
+// order_key of the largest of the 64 lanes' values; NaN is passed over.
+__device__ __forceinline__ int wave_max_key(float v) {
+  return wave_max(v != v ? kKeyNone : order_key(v));
+}
+
+// That value, -inf if there is none.
 __device__ __forceinline__ float wave_max_f(float v) {
-  constexpr int lo = (int)0xff800000u;                      // -inf
-#define MOONEP_MAXF(ctrl, rows) \
-  v = fmaxf(v, __int_as_float(MOONEP_DPP(lo, __float_as_int(v), ctrl, rows)))
-  MOONEP_MAXF(0x111, 0xf);
-  MOONEP_MAXF(0x112, 0xf);
-  MOONEP_MAXF(0x114, 0xf);
-  MOONEP_MAXF(0x118, 0xf);
-  MOONEP_MAXF(0x142, 0xa);
-  MOONEP_MAXF(0x143, 0xc);
-#undef MOONEP_MAXF
-  v = __int_as_float(wave_bcast(__float_as_int(v), kWave - 1));
-  return v != v ? -INFINITY : v;
+  const int k = wave_max_key(v);
+  return k == kKeyNone ? -INFINITY : key_value(k);
 }
 
 template <int P>
@@ -259,25 +256,26 @@ __device__ __forceinline__ int take_top(int (&key)[P], int K) {
 }
 
 // A bound t such that the K largest keys are among those >= t, and few others
-// are.  `top` is the lane's largest key, m the row's.  The K-th largest of the
-// 64 lanes' largest keys is such a bound; it is searched for on the scalar
-// unit, one comparison of the wave a step, first by doubling the distance to m
-// and then by halving the interval, until at most K + K/8 + 1 lanes reach it.
-// -inf where there is none above it (fewer than K lanes have a finite key).
-__device__ __forceinline__ float key_bound(float top, float m, int K) {
+// are.  `top` is the lane's largest key, `hi` the order_key of the row's.  The
+// K-th largest of the 64 lanes' largest keys is such a bound; it is searched
+// for on the scalar unit, one comparison of the wave a step, first by doubling
+// the distance to hi and then by halving the interval, until at most
+// K + K/8 + 1 lanes reach it.  -inf where there is none above it (fewer than K
+// lanes have a finite key).
+__device__ __forceinline__ float key_bound(float top, int hi, int K) {
   const int most = K + (K >> 3) + 1;
   const int low = order_key(-INFINITY);
-  int hi = __builtin_amdgcn_readfirstlane(order_key(m)), lo = hi, n = 0;
+  int lo = hi, n = 0;
   for (int d = 1 << 21;; d <<= 1) {
     if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
     lo -= d;
-    n = (int)__popcll(__ballot(top >= key_value(lo)));
+    n = (int)__popcll(ballot(top >= key_value(lo)));
     if (n >= K) break;
     hi = lo;
   }
   while (n > most && hi - lo > 1) {
     const int mid = lo + ((hi - lo) >> 1);
-    const int c = (int)__popcll(__ballot(top >= key_value(mid)));
+    const int c = (int)__popcll(ballot(top >= key_value(mid)));
     if (c >= K) {
       lo = mid;
       n = c;
@@ -288,57 +286,68 @@ __device__ __forceinline__ float key_bound(float top, float m, int K) {
   return key_value(lo);
 }
 
-// Inserts every key >= t (at most 64 of them, none NaN) into a list that lies
-// sorted across the lanes: lane k gets the k-th key and its expert, equal keys
-// in ascending expert.
-template <int P>
-__device__ __forceinline__ void insert_all(const float (&key)[P], float t, float& mykey,
-                                           int& mine) {
-  float lk = -INFINITY;
-  int li = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    uint64_t left = __ballot(key[i] >= t);
-    while (left) {
-      const int l = __ffsll((unsigned long long)left) - 1;
-      left &= left - 1;
-      const float v = __int_as_float(wave_bcast(__float_as_int(key[i]), l));
-      const int id = ((i >> 1) << 7) + 2 * l + (i & 1);
-      uint64_t before = __ballot(lk > v);
-      const uint64_t equal = __ballot(lk == v);
-      if (equal) before |= __ballot(lk == v && li < id);
-      const int pos = (int)__popcll(before);
-      const int uk = MOONEP_DPP(0, __float_as_int(lk), 0x138, 0xf);   // wave_shr:1
-      const int ui = MOONEP_DPP(0, li, 0x138, 0xf);
-      const bool stay = lane_id() < pos, here = lane_id() == pos;
-      lk = stay ? lk : here ? v : __int_as_float(uk);
-      li = stay ? li : here ? id : ui;
-    }
+// A list of (key, expert) that lies sorted across the lanes, largest first.
+// Inserting v moves the smaller keys one lane up: lane k then holds the median
+// of its own key, its lower neighbour's and v.  An equal key goes behind.
+struct LaneList {
+  float key = -INFINITY;
+  int id = 0x7fffffff;
+  __device__ __forceinline__ void insert(float v, int e) {
+    constexpr int inf = 0x7f800000;                         // below lane 0
+    const float up = __int_as_float(MOONEP_DPP(inf, __float_as_int(key), 0x138, 0xf));
+    const int ui = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xf, 0xf, true);   // wave_shr:1
+    id = key >= v ? id : up >= v ? e : ui;
+    key = __builtin_amdgcn_fmed3f(key, up, v);
   }
-  mykey = lk;
-  mine = li;
-}
+};
 
+// Lanes whose i-th key reaches t, for every i, and their number.
 template <int P>
-__device__ __forceinline__ int reaching(const float (&key)[P], float t) {
+__device__ __forceinline__ int reaching(const float (&key)[P], float t, uint64_t (&m)[P]) {
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < P; ++i) n += (int)__popcll(__ballot(key[i] >= t));
+  for (int i = 0; i < P; ++i) {
+    m[i] = ballot(key[i] >= t);
+    n += (int)__popcll(m[i]);
+  }
   return n;
 }
 
-// take_top through key_bound and insert_all.  False, and nothing done, where a
-// key is NaN or more keys than the list holds reach the bound.
+// The listed keys in a LaneList, inserted in ascending expert, so that equal
+// keys lie in that order too.
 template <int P>
-__device__ __forceinline__ bool insert_top(const float (&key)[P], float top, float m, int K,
-                                           float& mykey, int& mine) {
+__device__ __forceinline__ LaneList insert_all(const float (&key)[P], const uint64_t (&m)[P]) {
+  LaneList list;
+#pragma unroll
+  for (int i = 0; i < P; i += 2) {
+    uint64_t left = m[i] | m[i + 1];
+    while (left) {
+      const int l = __builtin_ctzll(left);
+      const uint64_t bit = left & -left;
+      left ^= bit;
+      const int e = ((i >> 1) << 7) + 2 * l;
+      if (m[i] & bit) list.insert(__int_as_float(wave_bcast(__float_as_int(key[i]), l)), e);
+      if (m[i + 1] & bit)
+        list.insert(__int_as_float(wave_bcast(__float_as_int(key[i + 1]), l)), e + 1);
+    }
+  }
+  return list;
+}
+
+// take_top through key_bound and insert_all: the largest keys, K at least.
+// False, and nothing done, where a key is NaN or more keys than the list holds
+// reach the bound.
+template <int P>
+__device__ __forceinline__ bool insert_top(const float (&key)[P], int K, LaneList& list) {
   uint64_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < P; i += 2) bad |= __ballot(__builtin_isunordered(key[i], key[i + 1]));
+  for (int i = 0; i < P; i += 2) bad |= ballot(__builtin_isunordered(key[i], key[i + 1]));
   if (bad) return false;
-  const float t = key_bound(top, m, K);
-  if (t == -INFINITY || reaching<P>(key, t) > kWave) return false;
-  insert_all<P>(key, t, mykey, mine);
+  const float top = lane_max<P>(key);
+  const float t = key_bound(top, wave_max_key(top), K);
+  uint64_t m[P];
+  if (t == -INFINITY || reaching<P>(key, t, m) > kWave) return false;
+  list = insert_all<P>(key, m);
   return true;
 }
 
@@ -429,28 +438,28 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, con
   const int64_t at = t * a.E;
   const bool soft = a.score == MOE_SCORE_SOFTMAX;
   const int n = a.K < a.E ? a.K + 1 : a.K;
-  float key[P], lk;
-  int id = 0;
+  float key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = fmaf(s[i], inv, bias[i]);
-  const float top = lane_max<P>(key);
-  bool listed = n <= kWave && insert_top<P>(key, top, wave_max_f(top), n, lk, id);
+  LaneList list;
+  bool listed = n <= kWave && insert_top<P>(key, n, list);
+  int id = list.id;
   float m = 0.f;                                         // only softmax looks at it
   if (soft) m = wave_max_f(lane_max<P>(z));
   if (listed) {
     const float err = soft ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
-    const float ko = __shfl_down(lk, 1, kWave);
+    const float lk = list.key, ko = __shfl_down(lk, 1, kWave);
     const bool apart = lk - ko > 2.f * err + 1.2e-7f * (fabsf(lk) + fabsf(ko));
-    if (!__all(lane >= n - 1 || apart)) {
+    if (ballot(lane < n - 1 && !apart)) {
       const float last = __int_as_float(wave_bcast(__float_as_int(lk), a.K - 1));
       const float reach = last - (2.f * err + 2.4e-7f * fabsf(last) + 1e-12f);
-      const int cnt = reaching<P>(key, reach);
+      uint64_t in[P];
+      const int cnt = reaching<P>(key, reach, in);
       listed = reach > -INFINITY && cnt <= kWave;
       if (listed) {
-        insert_all<P>(key, reach, lk, id);
+        id = insert_all<P>(key, in).id;
         const double sum = soft ? sum64<P, BF16>(a, at, (double)m) : 1.0;
-        const double mine =
-            lane < cnt ? key64<BF16>(a, at, id, (double)m, sum) : 0.0;
+        const double mine = lane < cnt ? key64<BF16>(a, at, id, (double)m, sum) : 0.0;
         int rank = 0;
         for (int j = 0; j < cnt; ++j) {
           const double kj = lane_bcast_d(mine, j);
@@ -471,13 +480,15 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, con
 template <int P, bool BF16>
 __device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
                                       float& zk) {
-  int id = 0;
-  const float top = lane_max<P>(z);
-  if (insert_top<P>(z, top, wave_max_f(top), a.K, zk, id)) return id;
+  LaneList list;
+  if (insert_top<P>(z, a.K, list)) {
+    zk = list.key;
+    return list.id;
+  }
   int key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
-  id = take_top<P>(key, a.K);
+  const int id = take_top<P>(key, a.K);
   zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
   return id;
 }
