@@ -186,40 +186,40 @@ __device__ __forceinline__ float recip(float sum) {          // 0 for an empty s
   return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
 }
 
-// Unnormalised shares p of a row in v (co: 1 - s for sigmoids) and their
-// factor.  The scores of a softmax are e^(z - shift) times that factor.  A row
-// whose every logit is -inf has p = 0.
-template <int P, bool CO>
-__device__ __forceinline__ float row_shares(const float (&z)[P], float (&v)[P], float (&co)[P],
-                                            bool soft, float& shift) {
+// Unnormalised shares p of token t in v (co: 1 - s for sigmoids) and their
+// factor, from its logits z.  The scores of a softmax are e^(z - shift) times
+// that factor.  A row whose every logit is -inf has p = 0.
+template <int P, bool BF16, bool FULL, bool SOFT, bool CO>
+__device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, const float (&z)[P],
+                                            float (&v)[P], float (&co)[P], float& shift) {
   float sum = 0.f;
   shift = 0.f;
-  if (soft) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+  for (int i = 0; i < P; ++i) {
+    if constexpr (SOFT) {
       v[i] = exp_f(z[i]);
-      sum += v[i];
-    }
-    sum = wave_sum_f(sum);
-    if (sum >= kPlainLo && sum <= kPlainHi) return recip(sum);
-  } else {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
+    } else {
       float c;
       v[i] = sigmoid_f(z[i], c);
       if constexpr (CO) co[i] = c;
-      sum += v[i];
     }
-    sum = wave_sum_f(sum);
-    if (sum >= kSigmoidLo) return recip(sum);
+    sum += v[i];
   }
-  const float m = wave_max_f(lane_max<P>(z));
-  if (!soft && !(m < kDeep)) return recip(sum);              // NaN, for one
+  sum = wave_sum_f(sum);
+  if (SOFT ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo) return recip(sum);
+  // the row is loaded again, so that z need not be kept for this
+  Row<P, BF16> again;
+  load_row<P, BF16, FULL>(a.logits, t, a.E, again);
+  float x[P];
+  unpack_row<P, BF16>(again, x);
+  const float m = wave_max_f(lane_max<P>(x));
+  if (!SOFT && !(m < kDeep)) return recip(sum);              // NaN, for one
   sum = 0.f;
   if (m > -INFINITY) shift = m;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    v[i] = exp_f(z[i] - shift);
+    v[i] = exp_f(x[i] - shift);
+    if constexpr (CO) co[i] = 1.f;                           // a deep row's 1 - s
     sum += v[i];
   }
   return recip(wave_sum_f(sum));
@@ -257,49 +257,49 @@ __device__ __forceinline__ int take_top(int (&key)[P], int K) {
 
 // A bound t such that the K largest keys are among those >= t, and few others
 // are.  `top` is the lane's largest key, `hi` the order_key of the row's.  The
-// K-th largest of the 64 lanes' largest keys is such a bound; it is searched
-// for on the scalar unit, one comparison of the wave a step, first by doubling
-// the distance to hi and then by halving the interval, until at most
-// K + K/8 + 1 lanes reach it.  -inf where there is none above it (fewer than K
-// lanes have a finite key).
-__device__ __forceinline__ float key_bound(float top, int hi, int K) {
-  const int most = K + (K >> 3) + 1;
+// K-th largest of the 64 lanes' largest keys is such a bound; any bound that K
+// to 3 K / 2 + 1 lanes reach is taken.  It is searched for on the scalar unit,
+// one comparison of the wave a step: from the bound of the wave's last token
+// (`probe`), whose row was much like this one, outwards by doubled steps and
+// then by halves.  -inf where there is none above it (fewer than K lanes have
+// a finite key).  The choice that follows does not depend on which is taken.
+__device__ __forceinline__ float key_bound(float top, int hi, int K, int& probe) {
+  const int most = K + (K >> 1) + 1;
   const int low = order_key(-INFINITY);
-  int lo = hi, n = 0;
-  for (int d = 1 << 21;; d <<= 1) {
-    if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
-    lo -= d;
-    n = (int)__popcll(ballot(top >= key_value(lo)));
-    if (n >= K) break;
-    hi = lo;
+  const auto reach = [&](int k) { return (int)__popcll(ballot(top >= key_value(k))); };
+  int lo = min(probe, hi), up = hi + 1, n = reach(lo);
+  if (n < K) {
+    for (int d = 1 << 18; n < K; d <<= 1) {
+      if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
+      up = lo;
+      lo -= d;
+      n = reach(lo);
+    }
+  } else if (n > most) {
+    for (int d = 1 << 18; d > 0 && hi - lo > d; d <<= 1) {
+      const int c = reach(lo + d);
+      if (c < K) {
+        up = lo + d;
+        break;
+      }
+      lo += d;
+      n = c;
+      if (n <= most) break;
+    }
   }
-  while (n > most && hi - lo > 1) {
-    const int mid = lo + ((hi - lo) >> 1);
-    const int c = (int)__popcll(ballot(top >= key_value(mid)));
+  while (n > most && up - lo > 1) {
+    const int mid = lo + (int)((uint32_t)(up - lo) >> 1);
+    const int c = reach(mid);
     if (c >= K) {
       lo = mid;
       n = c;
     } else {
-      hi = mid;
+      up = mid;
     }
   }
+  probe = lo;
   return key_value(lo);
 }
-
-// A list of (key, expert) that lies sorted across the lanes, largest first.
-// Inserting v moves the smaller keys one lane up: lane k then holds the median
-// of its own key, its lower neighbour's and v.  An equal key goes behind.
-struct LaneList {
-  float key = -INFINITY;
-  int id = 0x7fffffff;
-  __device__ __forceinline__ void insert(float v, int e) {
-    constexpr int inf = 0x7f800000;                         // below lane 0
-    const float up = __int_as_float(MOONEP_DPP(inf, __float_as_int(key), 0x138, 0xf));
-    const int ui = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xf, 0xf, true);   // wave_shr:1
-    id = key >= v ? id : up >= v ? e : ui;
-    key = __builtin_amdgcn_fmed3f(key, up, v);
-  }
-};
 
 // Lanes whose i-th key reaches t, for every i, and their number.
 template <int P>
@@ -313,41 +313,85 @@ __device__ __forceinline__ int reaching(const float (&key)[P], float t, uint64_t
   return n;
 }
 
-// The listed keys in a LaneList, inserted in ascending expert, so that equal
-// keys lie in that order too.
-template <int P>
-__device__ __forceinline__ LaneList insert_all(const float (&key)[P], const uint64_t (&m)[P]) {
-  LaneList list;
-#pragma unroll
-  for (int i = 0; i < P; i += 2) {
-    uint64_t left = m[i] | m[i + 1];
-    while (left) {
-      const int l = __builtin_ctzll(left);
-      const uint64_t bit = left & -left;
-      left ^= bit;
-      const int e = ((i >> 1) << 7) + 2 * l;
-      if (m[i] & bit) list.insert(__int_as_float(wave_bcast(__float_as_int(key[i]), l)), e);
-      if (m[i + 1] & bit)
-        list.insert(__int_as_float(wave_bcast(__float_as_int(key[i + 1]), l)), e + 1);
-    }
-  }
-  return list;
+// A wave's list of up to 64 keys and their experts.
+struct KeyList {
+  float key[kWave];
+  int id[kWave];
+};
+
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// take_top through key_bound and insert_all: the largest keys, K at least.
-// False, and nothing done, where a key is NaN or more keys than the list holds
-// reach the bound.
+// Sorts the cnt <= 64 keys that m marks across the lanes, largest first, equal
+// ones in ascending expert: lane k < cnt gets the k-th key and its expert.
+// They are written to the list in ascending expert, and each lane counts the
+// keys that come before its own (a broadcast read of four keys at a time);
+// that place is where it sends them.
 template <int P>
-__device__ __forceinline__ bool insert_top(const float (&key)[P], int K, LaneList& list) {
+__device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_t (&m)[P],
+                                            int cnt, KeyList& list, float& mykey, int& mine) {
+  const int lane = lane_id();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < P; i += 2) {
+    if ((m[i] | m[i + 1]) == 0) continue;
+    int at = base;
+    at = __builtin_amdgcn_mbcnt_lo((uint32_t)m[i], at);
+    at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i] >> 32), at);
+    at = __builtin_amdgcn_mbcnt_lo((uint32_t)m[i + 1], at);
+    at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i + 1] >> 32), at);
+    const bool first = __builtin_amdgcn_inverse_ballot_w64(m[i]);
+    if (first) {
+      list.key[at] = key[i];
+      list.id[at] = expert_of(i);
+    }
+    if (__builtin_amdgcn_inverse_ballot_w64(m[i + 1])) {
+      const int to = at + (first ? 1 : 0);
+      list.key[to] = key[i + 1];
+      list.id[to] = expert_of(i + 1);
+    }
+    base += (int)__popcll(m[i]) + (int)__popcll(m[i + 1]);
+  }
+  if (lane >= cnt) list.key[lane] = -INFINITY;
+  wave_lds_fence();
+  const float k = list.key[lane];
+  const int id = list.id[lane];
+  int rank = 0;
+  for (int j = 0; j < cnt; j += 4) {
+    const f32x4 o = *reinterpret_cast<const f32x4*>(list.key + j);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t later = ~uint64_t(1) << (j + q);        // lanes after j + q
+      const uint64_t before = ballot(o[q] > k) | (ballot(o[q] == k) & later);
+      rank += __builtin_amdgcn_inverse_ballot_w64(before) ? 1 : 0;
+    }
+  }
+  wave_lds_fence();                              // the list is written again
+  const int to = 4 * (lane < cnt ? rank : lane);
+  mykey = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(k)));
+  mine = __builtin_amdgcn_ds_permute(to, id);
+}
+
+// take_top through key_bound and sort_marked: the largest keys, K at least.
+// False, and nothing done, where a key is NaN or more than 64 keys reach the
+// bound.
+template <int P>
+__device__ __forceinline__ bool sort_top(const float (&key)[P], int K, int& probe, KeyList& list,
+                                         float& mykey, int& mine) {
   uint64_t bad = 0;
 #pragma unroll
   for (int i = 0; i < P; i += 2) bad |= ballot(__builtin_isunordered(key[i], key[i + 1]));
   if (bad) return false;
   const float top = lane_max<P>(key);
-  const float t = key_bound(top, wave_max_key(top), K);
+  const float t = key_bound(top, wave_max_key(top), K, probe);
   uint64_t m[P];
-  if (t == -INFINITY || reaching<P>(key, t, m) > kWave) return false;
-  list = insert_all<P>(key, m);
+  if (t == -INFINITY) return false;
+  const int cnt = reaching<P>(key, t, m);
+  if (cnt > kWave) return false;
+  sort_marked<P>(key, m, cnt, list, mykey, mine);
   return true;
 }
 
@@ -430,25 +474,22 @@ __device__ int take_top64(const RouterArgs& a, int64_t at, double m, double sum)
 //            (2.2 ln E + 48 + 33) h:  <= 8e-6 p_max,
 // and by h |key| from the addition.  Other rows list every key that may be
 // among the K largest, at most 64, and order those in float64, a lane each.
-template <int P, bool BF16>
-__device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, const float (&z)[P],
+template <int P, bool BF16, bool SOFT>
+__device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, float m,
                                              const float (&s)[P], const float (&bias)[P],
-                                             float inv, float shift, float& zk) {
+                                             float inv, float shift, int& probe, KeyList& list,
+                                             float& zk) {
   const int lane = lane_id();
   const int64_t at = t * a.E;
-  const bool soft = a.score == MOE_SCORE_SOFTMAX;
   const int n = a.K < a.E ? a.K + 1 : a.K;
-  float key[P];
+  float key[P], lk = 0.f;
+  int id = 0;
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = fmaf(s[i], inv, bias[i]);
-  LaneList list;
-  bool listed = n <= kWave && insert_top<P>(key, n, list);
-  int id = list.id;
-  float m = 0.f;                                         // only softmax looks at it
-  if (soft) m = wave_max_f(lane_max<P>(z));
+  bool listed = n <= kWave && sort_top<P>(key, n, probe, list, lk, id);
   if (listed) {
-    const float err = soft ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
-    const float lk = list.key, ko = __shfl_down(lk, 1, kWave);
+    const float err = SOFT ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
+    const float ko = __shfl_down(lk, 1, kWave);
     const bool apart = lk - ko > 2.f * err + 1.2e-7f * (fabsf(lk) + fabsf(ko));
     if (ballot(lane < n - 1 && !apart)) {
       const float last = __int_as_float(wave_bcast(__float_as_int(lk), a.K - 1));
@@ -457,8 +498,8 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, con
       const int cnt = reaching<P>(key, reach, in);
       listed = reach > -INFINITY && cnt <= kWave;
       if (listed) {
-        id = insert_all<P>(key, in).id;
-        const double sum = soft ? sum64<P, BF16>(a, at, (double)m) : 1.0;
+        sort_marked<P>(key, in, cnt, list, lk, id);
+        const double sum = SOFT ? sum64<P, BF16>(a, at, (double)m) : 1.0;
         const double mine = lane < cnt ? key64<BF16>(a, at, id, (double)m, sum) : 0.0;
         int rank = 0;
         for (int j = 0; j < cnt; ++j) {
@@ -471,7 +512,7 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, con
     }
   }
   if (!listed)
-    id = take_top64<P, BF16>(a, at, (double)m, soft ? sum64<P, BF16>(a, at, (double)m) : 1.0);
+    id = take_top64<P, BF16>(a, at, (double)m, SOFT ? sum64<P, BF16>(a, at, (double)m) : 1.0);
   zk = logit_at<BF16>(a.logits, at + (lane < a.K ? id : 0));
   return id;
 }
@@ -479,33 +520,31 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, con
 // Lane k < K: the k-th expert by logit, and its logit zk.
 template <int P, bool BF16>
 __device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
-                                      float& zk) {
-  LaneList list;
-  if (insert_top<P>(z, a.K, list)) {
-    zk = list.key;
-    return list.id;
-  }
+                                      int& probe, KeyList& list, float& zk) {
+  int id = 0;
+  if (sort_top<P>(z, a.K, probe, list, zk, id)) return id;
   int key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
-  const int id = take_top<P>(key, a.K);
+  id = take_top<P>(key, a.K);
   zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
   return id;
 }
 
 // Lane k < K (`on`): the gate of the chosen logit zk, over scale.
-__device__ __forceinline__ float gate_share(float zk, bool on, bool soft, bool renorm, float shift,
+template <bool SOFT>
+__device__ __forceinline__ float gate_share(float zk, bool on, bool renorm, float shift,
                                             float inv) {
   if (!renorm) {
     if (!on) return 0.f;
-    return soft ? exp_f(zk - shift) * inv : sigmoid_f(zk);
+    return SOFT ? exp_f(zk - shift) * inv : sigmoid_f(zk);
   }
-  float s = on ? soft ? exp_f(zk) : sigmoid_f(zk) : 0.f;
+  float s = on ? SOFT ? exp_f(zk) : sigmoid_f(zk) : 0.f;
   float sum = wave_sum_f(s);
-  const bool plain = soft ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo;
+  const bool plain = SOFT ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo;
   if (!plain) {
     const float mk = wave_max_f(on ? zk : -INFINITY);
-    if (soft || mk < kDeep) {
+    if (SOFT || mk < kDeep) {
       s = on ? exp_f(mk > -INFINITY ? zk - mk : zk) : 0.f;
       sum = wave_sum_f(s);
     }
@@ -542,12 +581,14 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // workspace when the sequence or the chunk ends.  Along the tokens either
 // number grows, so no two pieces share a row.
 // ---------------------------------------------------------------------------
-template <int P, bool BF16, bool FULL, bool SELECT, bool BIAS, bool STATS>
+template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
 __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
   extern __shared__ float lds[];                  // [waves][E] sums, [E] counts
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
-  const bool soft = a.score == MOE_SCORE_SOFTMAX;
+  __shared__ __attribute__((aligned(16))) KeyList lists[SELECT ? kRtWaves : 1];
+  KeyList& list = lists[SELECT ? wv : 0];
+  int probe = 0;                                  // order_key of 0
   int* cnt = reinterpret_cast<int*>(lds + kRtWaves * E);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   float acc[P], bias[P];
@@ -577,8 +618,8 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
           if (lane < K) id = a.ids[int64_t(t) * K + lane];
         }
         float inv = 1.f, shift = 0.f;
-        if (STATS || (SELECT && soft && (BIAS || !a.renorm)))
-          inv = row_shares<P, false>(z, v, co, soft, shift);
+        if (STATS || (SELECT && SOFT && (BIAS || !a.renorm)))
+          inv = row_shares<P, BF16, FULL, SOFT, false>(a, t, z, v, co, shift);
         if constexpr (STATS) {
           if (seq >= 0) {
 #pragma unroll
@@ -588,16 +629,19 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
         if constexpr (SELECT) {
           float zk;
           if constexpr (BIAS) {
-            if (!soft && (!STATS || shift != 0.f)) {      // v holds no sigmoids
+            float m = 0.f;
+            if constexpr (SOFT) m = wave_max_f(lane_max<P>(z));
+            if (!SOFT && (!STATS || shift != 0.f)) {      // v holds no sigmoids
 #pragma unroll
               for (int i = 0; i < P; ++i) v[i] = sigmoid_f(z[i]);
             }
-            id = choose_biased<P, BF16>(a, t, z, v, bias, soft ? inv : 1.f, shift, zk);
+            id = choose_biased<P, BF16, SOFT>(a, t, m, v, bias, SOFT ? inv : 1.f, shift, probe,
+                                              list, zk);
           } else {
-            id = choose<P, BF16>(a, t, z, zk);
+            id = choose<P, BF16>(a, t, z, probe, list, zk);
           }
           const bool on = lane < K;
-          const float w = gate_share(zk, on, soft, a.renorm, shift, inv);
+          const float w = gate_share<SOFT>(zk, on, a.renorm, shift, inv);
           if (on) {
             a.ids[int64_t(t) * K + lane] = id;
             a.gates[int64_t(t) * K + lane] = a.scale * w;
@@ -713,15 +757,14 @@ __global__ __launch_bounds__(kWave) void k_router_loss(RouterArgs a, const int32
 // These K values reach the lanes that hold their experts through an LDS row.
 // A gradient of renormalised gates alone reads only the K chosen logits.
 // ---------------------------------------------------------------------------
-template <int P, bool BF16, bool FULL>
+template <int P, bool BF16, bool FULL, bool SOFT>
 __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
   extern __shared__ float lds[];                  // [waves][64 P]
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
   float* row = lds + wv * (64 * P);
-  const bool soft = a.score == MOE_SCORE_SOFTMAX;
   const bool balance = a.dloss != nullptr, gates = a.dgates != nullptr;
-  const bool into_u = soft && gates && !a.renorm;         // the gates' part goes through p
+  const bool into_u = SOFT && gates && !a.renorm;         // the gates' part goes through p
   if (gates) {
 #pragma unroll
     for (int i = 0; i < P; i += 2) *reinterpret_cast<float2*>(row + expert_of(i)) = float2{0, 0};
@@ -749,11 +792,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
       float z[P];
       unpack_row<P, BF16>(next, z);
       if (t + 1 < t1) load_row<P, BF16, FULL>(a.logits, t + 1, E, next);
-      inv = row_shares<P, true>(z, v, co, soft, shift);
-      if (!soft && shift != 0.f) {                // deep row: v is not s, but 1 - s is 1
-#pragma unroll
-        for (int i = 0; i < P; ++i) co[i] = 1.f;
-      }
+      inv = row_shares<P, BF16, FULL, SOFT, !SOFT>(a, t, z, v, co, shift);
     }
     const int id = next_id;
     const bool on = (unsigned)id < (unsigned)E;
@@ -779,27 +818,23 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
     if (gates) {
       if (!into_u) {
         const float zk = on ? logit_at<BF16>(a.logits, int64_t(t) * E + id) : 0.f;
-        const float w = gate_share(zk, on, soft, a.renorm, shift, inv);
+        const float w = gate_share<SOFT>(zk, on, a.renorm, shift, inv);
         dg = w * (dg - (a.renorm ? wave_sum_f(dg * w) : 0.f));
-        if (!soft) {
+        if constexpr (!SOFT) {
           float c;
           sigmoid_f(zk, c);
           dg *= c;
         }
       }
       if (on) atomicAdd(&row[id], dg);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_lds_fence();
 #pragma unroll
       for (int i = 0; i < P; i += 2) {
         const float2 g = *reinterpret_cast<const float2*>(row + expert_of(i));
         dz[i] = g.x;
         dz[i + 1] = g.y;
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_lds_fence();
       if (on) row[id] = 0.f;
     } else {
 #pragma unroll
@@ -821,7 +856,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
       if (into_u) {
 #pragma unroll
         for (int i = 0; i < P; ++i) dz[i] = v[i] * inv * (dz[i] - mean);
-      } else if (soft) {
+      } else if constexpr (SOFT) {
 #pragma unroll
         for (int i = 0; i < P; ++i) dz[i] = fmaf(v[i] * inv, u[i] - mean, dz[i]);
       } else {
@@ -933,13 +968,22 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
       constexpr int P = decltype(p)::value;
       constexpr bool BF = decltype(b)::value, FULL = decltype(full)::value;
       const dim3 g(grid), t(kRtThreads);
-#define MOE_ROUTER(SEL, BIAS, STATS) \
-  hipLaunchKernelGGL((k_router<P, BF, FULL, SEL, BIAS, STATS>), g, t, lds, stream, a)
-      if (!select) MOE_ROUTER(false, false, true);
-      else if (stats && a.bias) MOE_ROUTER(true, true, true);
-      else if (stats) MOE_ROUTER(true, false, true);
-      else if (a.bias) MOE_ROUTER(true, true, false);
-      else MOE_ROUTER(true, false, false);
+#define MOE_ROUTER(SEL, BIAS, STATS)                                                           \
+  if (a.score == MOE_SCORE_SOFTMAX)                                                            \
+    hipLaunchKernelGGL((k_router<P, BF, FULL, true, SEL, BIAS, STATS>), g, t, lds, stream, a); \
+  else                                                                                         \
+    hipLaunchKernelGGL((k_router<P, BF, FULL, false, SEL, BIAS, STATS>), g, t, lds, stream, a)
+      if (!select) {
+        MOE_ROUTER(false, false, true);
+      } else if (stats && a.bias) {
+        MOE_ROUTER(true, true, true);
+      } else if (stats) {
+        MOE_ROUTER(true, false, true);
+      } else if (a.bias) {
+        MOE_ROUTER(true, true, false);
+      } else {
+        MOE_ROUTER(true, false, false);
+      }
 #undef MOE_ROUTER
       return hip_status();
     });
@@ -1041,8 +1085,12 @@ extern "C" int moe_router_backward(const moe_cfg* cfg, const moe_router_cfg* rcf
   return with_row(a.E, rcfg->logits_bf16, [&](auto p, auto b, auto full) {
     constexpr int P = decltype(p)::value;
     const size_t lds = dgates ? size_t(kRtWaves) * 64 * P * 4 : 0;
-    hipLaunchKernelGGL((k_router_bwd<P, decltype(b)::value, decltype(full)::value>),
-                       dim3((a.T + per - 1) / per), dim3(kRtThreads), lds, stream, a);
+    constexpr bool BF = decltype(b)::value, FULL = decltype(full)::value;
+    const dim3 grid((a.T + per - 1) / per), block(kRtThreads);
+    if (a.score == MOE_SCORE_SOFTMAX)
+      hipLaunchKernelGGL((k_router_bwd<P, BF, FULL, true>), grid, block, lds, stream, a);
+    else
+      hipLaunchKernelGGL((k_router_bwd<P, BF, FULL, false>), grid, block, lds, stream, a);
     return hip_status();
   });
 }
