@@ -267,16 +267,18 @@ __device__ __forceinline__ float key_bound(float top, int hi, int K, int& probe)
   const int most = K + (K >> 1) + 1;
   const int low = order_key(-INFINITY);
   const auto reach = [&](int k) { return (int)__popcll(ballot(top >= key_value(k))); };
-  int lo = min(probe, hi), up = hi + 1, n = reach(lo);
+  const bool fresh = probe == kKeyNone;                      // no token before
+  const int step = fresh ? 1 << 20 : 1 << 18;
+  int lo = fresh ? max(hi - step, low + 1) : min(probe, hi), up = hi + 1, n = reach(lo);
   if (n < K) {
-    for (int d = 1 << 18; n < K; d <<= 1) {
+    for (int d = step; n < K; d <<= 1) {
       if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
       up = lo;
       lo -= d;
       n = reach(lo);
     }
   } else if (n > most) {
-    for (int d = 1 << 18; d > 0 && hi - lo > d; d <<= 1) {
+    for (int d = step; d > 0 && hi - lo > d; d <<= 1) {
       const int c = reach(lo + d);
       if (c < K) {
         up = lo + d;
@@ -395,55 +397,67 @@ __device__ __forceinline__ bool sort_top(const float (&key)[P], int K, int& prob
   return true;
 }
 
-// Score plus bias of one expert in float64.
-template <bool BF16>
+// Score plus bias of one expert in float64; at: the row's first logit.
+template <bool BF16, bool SOFT>
 __device__ __forceinline__ double key64(const RouterArgs& a, int64_t at, int e, double m,
                                         double sum) {
   const double z = (double)logit_at<BF16>(a.logits, at + e);
   double s;
-  if (a.score == MOE_SCORE_SOFTMAX) s = m == -INFINITY && z == z ? 0.0 : exp(z - m) / sum;
+  if constexpr (SOFT) s = m == -INFINITY && z == z ? 0.0 : exp(z - m) / sum;
   else s = 1.0 / (1.0 + exp(-z));
   return s + (double)a.bias[e];
 }
 
 // Sum of a row's e^(z - m) in float64.
-template <int P, bool BF16>
-__device__ double sum64(const RouterArgs& a, int64_t at, double m) {
+template <bool BF16>
+__device__ __forceinline__ double sum64(const RouterArgs& a, int64_t at, double m) {
   double sum = 0.0;
-  for (int i = 0; i < P; ++i) {
-    const int e = expert_of(i);
-    if (e < a.E) {
-      const double z = (double)logit_at<BF16>(a.logits, at + e);
-      if (!(m == -INFINITY && z == z)) sum += exp(z - m);
-    }
+#pragma unroll 1
+  for (int e = lane_id(); e < a.E; e += kWave) {
+    const double z = (double)logit_at<BF16>(a.logits, at + e);
+    if (!(m == -INFINITY && z == z)) sum += exp(z - m);
   }
   return wave_sum_d(sum);
+}
+
+// Orders the cnt experts `id` of lanes 0 .. cnt - 1 by float64 score plus bias.
+template <bool BF16, bool SOFT>
+__device__ __forceinline__ int order64(const RouterArgs& a, int64_t at, float mf, int cnt, int id) {
+  const int lane = lane_id();
+  const double m = (double)mf, sum = SOFT ? sum64<BF16>(a, at, m) : 1.0;
+  const double mine = lane < cnt ? key64<BF16, SOFT>(a, at, id, m, sum) : 0.0;
+  int rank = 0;
+  for (int j = 0; j < cnt; ++j) {
+    const double kj = lane_bcast_d(mine, j);
+    const int ij = wave_bcast(id, j);
+    rank += kj > mine || (kj == mine && ij < id) ? 1 : 0;
+  }
+  return __builtin_amdgcn_ds_permute(4 * (lane < cnt ? rank : lane), id);
 }
 
 // take_top on the float64 scores plus bias: the K largest, equal ones in
 // ascending expert, NaN last.  For rows that nothing else orders (NaN, more
 // than 64 keys near each other), so nothing is kept in registers between
 // rounds: the scores are computed anew.
-template <int P, bool BF16>
-__device__ int take_top64(const RouterArgs& a, int64_t at, double m, double sum) {
+template <bool BF16, bool SOFT>
+__device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float mf) {
   const int lane = lane_id();
-  uint32_t taken = 0;                            // P <= 32 bits
+  const double m = (double)mf, sum = SOFT ? sum64<BF16>(a, at, m) : 1.0;
+  uint32_t taken = 0;                            // at most 32 experts a lane
   int mine = 0;
   for (int k = 0; k < a.K; ++k) {
     // class of a candidate: 2 a number, 1 NaN, 0 none
     double best = 0.0;
-    int cls = 0, id = 0x7fffffff, bi = 0;
+    int cls = 0, id = 0x7fffffff;
 #pragma unroll 1
-    for (int i = 0; i < P; ++i) {
-      const int e = expert_of(i);
-      if (e >= a.E || (taken >> i & 1)) continue;
-      const double d = key64<BF16>(a, at, e, m, sum);
+    for (int i = 0, e = lane; e < a.E; ++i, e += kWave) {
+      if (taken >> i & 1) continue;
+      const double d = key64<BF16, SOFT>(a, at, e, m, sum);
       const int c = d == d ? 2 : 1;
       if (c > cls || (c == cls && c == 2 && d > best)) {
         cls = c;
         best = d;
         id = e;
-        bi = i;
       }
     }
     const int myid = id;
@@ -457,7 +471,7 @@ __device__ int take_top64(const RouterArgs& a, int64_t at, double m, double sum)
         id = oi;
       }
     }
-    if (id == myid && cls > 0) taken |= 1u << bi;
+    if (id == myid && cls > 0) taken |= 1u << (id / kWave);
     if (lane == k) mine = id;
   }
   return mine;
@@ -499,20 +513,11 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, flo
       listed = reach > -INFINITY && cnt <= kWave;
       if (listed) {
         sort_marked<P>(key, in, cnt, list, lk, id);
-        const double sum = SOFT ? sum64<P, BF16>(a, at, (double)m) : 1.0;
-        const double mine = lane < cnt ? key64<BF16>(a, at, id, (double)m, sum) : 0.0;
-        int rank = 0;
-        for (int j = 0; j < cnt; ++j) {
-          const double kj = lane_bcast_d(mine, j);
-          const int ij = wave_bcast(id, j);
-          rank += kj > mine || (kj == mine && ij < id) ? 1 : 0;
-        }
-        id = __builtin_amdgcn_ds_permute(4 * (lane < cnt ? rank : lane), id);
+        id = order64<BF16, SOFT>(a, at, m, cnt, id);
       }
     }
   }
-  if (!listed)
-    id = take_top64<P, BF16>(a, at, (double)m, SOFT ? sum64<P, BF16>(a, at, (double)m) : 1.0);
+  if (!listed) id = take_top64<BF16, SOFT>(a, at, m);
   zk = logit_at<BF16>(a.logits, at + (lane < a.K ? id : 0));
   return id;
 }
@@ -588,7 +593,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
   const int E = a.E, K = a.K;
   __shared__ __attribute__((aligned(16))) KeyList lists[SELECT ? kRtWaves : 1];
   KeyList& list = lists[SELECT ? wv : 0];
-  int probe = 0;                                  // order_key of 0
+  int probe = kKeyNone;
   int* cnt = reinterpret_cast<int*>(lds + kRtWaves * E);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
   float acc[P], bias[P];
@@ -730,18 +735,25 @@ __global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int 
   }
 }
 
-// The loss of a sequence from its counts and P: one wave.
-__global__ __launch_bounds__(kWave) void k_router_loss(RouterArgs a, const int32_t* counts,
-                                                       const float* prob, float* loss) {
+// The loss of a sequence from its counts and P.
+constexpr int kLossThreads = 512;
+
+__global__ __launch_bounds__(kLossThreads) void k_router_loss(RouterArgs a, const int32_t* counts,
+                                                              const float* prob, float* loss) {
+  __shared__ double part[kLossThreads / kWave];
   const int seq = blockIdx.x;
   const int lo = a.cu ? max(0, min(a.cu[seq], a.T)) : 0;
   const int hi = a.cu ? max(lo, min(a.cu[seq + 1], a.T)) : a.T;
-  double total = 0.0;
-  for (int e = lane_id(); e < a.E; e += kWave)
-    total += (double)counts[int64_t(seq) * a.E + e] * (double)prob[int64_t(seq) * a.E + e];
-  total = wave_sum_d(total);
-  if (lane_id() == 0)
-    loss[seq] = hi > lo ? (float)(total * a.E / ((double)a.K * (hi - lo))) : 0.f;
+  double f = 0.0;
+  for (int e = threadIdx.x; e < a.E; e += kLossThreads)
+    f += (double)counts[int64_t(seq) * a.E + e] * (double)prob[int64_t(seq) * a.E + e];
+  f = wave_sum_d(f);
+  if (lane_id() == 0) part[threadIdx.x / kWave] = f;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kLossThreads / kWave; ++w) f += part[w];
+    loss[seq] = hi > lo ? (float)(f * a.E / ((double)a.K * (hi - lo))) : 0.f;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -995,7 +1007,7 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
     hipLaunchKernelGGL(k_router_join, dim3(a.nseq, one ? 1 : slices), dim3(kJoinThreads), 0, stream,
                        a, chunks, one ? slices : 1, counts, prob, loss);
     if (!one && slices > 1)
-      hipLaunchKernelGGL(k_router_loss, dim3(a.nseq), dim3(kWave), 0, stream, a, counts, prob,
+      hipLaunchKernelGGL(k_router_loss, dim3(a.nseq), dim3(kLossThreads), 0, stream, a, counts, prob,
                          loss);
     return hip_status();
   }
