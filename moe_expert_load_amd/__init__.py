@@ -144,12 +144,19 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on_device(*tensors):
-    """Refuse tensors of another GPU than the current one (the launch's)."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, here))
+def _arg(t, dtype, numel, name, device):
+    """Address of a tensor that a kernel on `device` (the current one) may use.
+
+    The checks and errors of _ptr, in one pass over cheap attributes: a
+    decode-size call lasts only a few microseconds on the GPU.
+    """
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device
+            or t.numel() < numel or not t.is_contiguous()):
+        _ptr(t, dtype, numel, name)
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, device))
+    return t.data_ptr()
 
 
 def moe_strerror(code):
@@ -388,124 +395,134 @@ def moe_router_workspace_size(cfg, rcfg):
     return int(out.value)
 
 
-def _logits(cfg, rcfg, t, name):
-    return _ptr(t, torch.bfloat16 if rcfg.logits_bf16 else torch.float32,
-                cfg.R * cfg.S * cfg.E, name)
-
-
-def _loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace):
-    n = rcfg.nseq
-    return (_ptr(cu_tokens, torch.int32, n + 1, "cu_tokens"),
-            _ptr(counts, torch.int32, n * cfg.E, "counts"),
-            _ptr(prob, torch.float32, n * cfg.E, "prob"),
-            _ptr(loss, torch.float32, n, "loss"),
-            _ptr(workspace, torch.uint8,
-                 moe_router_workspace_size(cfg, rcfg) if loss is not None else None, "workspace"))
+def _loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace, dev):
+    n, m = rcfg.nseq, rcfg.nseq * cfg.E
+    return (_arg(cu_tokens, torch.int32, n + 1, "cu_tokens", dev),
+            _arg(counts, torch.int32, m, "counts", dev),
+            _arg(prob, torch.float32, m, "prob", dev),
+            _arg(loss, torch.float32, n, "loss", dev),
+            _arg(workspace, torch.uint8, moe_router_workspace_size(cfg, rcfg), "workspace", dev))
 
 
 def moe_router(cfg, rcfg, logits, bias, topk_ids, gates, cu_tokens=None, counts=None, prob=None,
                loss=None, workspace=None, stream=None):
     """Ids and gates; with counts, prob, loss and workspace the balance loss too."""
-    n = cfg.R * cfg.S * cfg.K
-    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
-            _ptr(bias, torch.float32, cfg.E, "bias"),
-            _ptr(topk_ids, torch.int32, n, "topk_ids"),
-            _ptr(gates, torch.float32, n, "gates"),
-            *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace))
-    _on_device(logits, bias, topk_ids, gates, cu_tokens, counts, prob, loss, workspace)
-    _check(load().moe_router(*args, _stream(stream)), "moe_router")
+    dev = torch.cuda.current_device()
+    T = cfg.R * cfg.S
+    rest = (None,) * 5
+    if loss is not None or counts is not None or prob is not None:
+        rest = _loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace, dev)
+    _check(load().moe_router(
+        ctypes.byref(cfg), ctypes.byref(rcfg),
+        _arg(logits, torch.bfloat16 if rcfg.logits_bf16 else torch.float32, T * cfg.E, "logits",
+             dev),
+        _arg(bias, torch.float32, cfg.E, "bias", dev),
+        _arg(topk_ids, torch.int32, T * cfg.K, "topk_ids", dev),
+        _arg(gates, torch.float32, T * cfg.K, "gates", dev),
+        *rest, _stream(stream)), "moe_router")
 
 
 def moe_balance_loss(cfg, rcfg, logits, topk_ids, cu_tokens, counts, prob, loss, workspace,
                      stream=None):
-    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
-            _ptr(topk_ids, torch.int32, cfg.R * cfg.S * cfg.K, "topk_ids"),
-            *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace))
-    _on_device(logits, topk_ids, cu_tokens, counts, prob, loss, workspace)
-    _check(load().moe_balance_loss(*args, _stream(stream)), "moe_balance_loss")
+    dev = torch.cuda.current_device()
+    T = cfg.R * cfg.S
+    _check(load().moe_balance_loss(
+        ctypes.byref(cfg), ctypes.byref(rcfg),
+        _arg(logits, torch.bfloat16 if rcfg.logits_bf16 else torch.float32, T * cfg.E, "logits",
+             dev),
+        _arg(topk_ids, torch.int32, T * cfg.K, "topk_ids", dev),
+        *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace, dev),
+        _stream(stream)), "moe_balance_loss")
 
 
 def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits,
                         stream=None):
     """dgates or dloss (with counts and cu_tokens) may be None."""
-    n = cfg.R * cfg.S * cfg.K
-    args = (ctypes.byref(cfg), ctypes.byref(rcfg), _logits(cfg, rcfg, logits, "logits"),
-            _ptr(topk_ids, torch.int32, n, "topk_ids"),
-            _ptr(dgates, torch.float32, n, "dgates"),
-            _ptr(cu_tokens, torch.int32, rcfg.nseq + 1, "cu_tokens"),
-            _ptr(counts, torch.int32, rcfg.nseq * cfg.E, "counts"),
-            _ptr(dloss, torch.float32, rcfg.nseq, "dloss"),
-            _logits(cfg, rcfg, dlogits, "dlogits"))
-    _on_device(logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits)
-    _check(load().moe_router_backward(*args, _stream(stream)), "moe_router_backward")
+    dev = torch.cuda.current_device()
+    T, n = cfg.R * cfg.S, rcfg.nseq
+    dtype = torch.bfloat16 if rcfg.logits_bf16 else torch.float32
+    _check(load().moe_router_backward(
+        ctypes.byref(cfg), ctypes.byref(rcfg),
+        _arg(logits, dtype, T * cfg.E, "logits", dev),
+        _arg(topk_ids, torch.int32, T * cfg.K, "topk_ids", dev),
+        _arg(dgates, torch.float32, T * cfg.K, "dgates", dev),
+        _arg(cu_tokens, torch.int32, n + 1, "cu_tokens", dev),
+        _arg(counts, torch.int32, n * cfg.E, "counts", dev),
+        _arg(dloss, torch.float32, n, "dloss", dev),
+        _arg(dlogits, dtype, T * cfg.E, "dlogits", dev), _stream(stream)), "moe_router_backward")
 
 
-def _kept(rows, width, q, scale, what):
+def _kept(rows, width, q, scale, what, dev):
     """Codes and scale bytes of `rows` rows of `width` values."""
-    return (_ptr(q, torch.uint8, rows * width, what + " codes"),
-            _ptr(scale, torch.uint8, rows * ((width + 31) // 32), what + " scales"))
+    return (_arg(q, torch.uint8, rows * width, what + " codes", dev),
+            _arg(scale, torch.uint8, rows * ((width + 31) // 32), what + " scales", dev))
 
 
 def moe_q8_store(rows, width, src, q, scale, stream=None):
     """Codes q [rows, width] and scale bytes [rows, ceil(width / 32)] of bf16 rows."""
-    a = _ptr(src, torch.bfloat16, rows * width, "src")
-    kept = _kept(rows, width, q, scale, "q8")
-    _on_device(src, q, scale)
-    _check(load().moe_q8_store(rows, width, a, *kept, _stream(stream)), "moe_q8_store")
+    dev = torch.cuda.current_device()
+    _check(load().moe_q8_store(rows, width,
+                               _arg(src, torch.bfloat16, rows * width, "src", dev),
+                               *_kept(rows, width, q, scale, "q8", dev), _stream(stream)),
+           "moe_q8_store")
 
 
 def moe_q8_load(rows, width, q, scale, dst, stream=None):
-    kept = _kept(rows, width, q, scale, "q8")
-    o = _ptr(dst, torch.bfloat16, rows * width, "dst")
-    _on_device(q, scale, dst)
-    _check(load().moe_q8_load(rows, width, *kept, o, _stream(stream)), "moe_q8_load")
+    dev = torch.cuda.current_device()
+    _check(load().moe_q8_load(rows, width, *_kept(rows, width, q, scale, "q8", dev),
+                              _arg(dst, torch.bfloat16, rows * width, "dst", dev),
+                              _stream(stream)), "moe_q8_load")
 
 
 def moe_dispatch_q8(cfg, plan, xq, xscale, xperm, stream=None):
+    dev = torch.cuda.current_device()
     ntok = cfg.R * cfg.S
-    kept = _kept(ntok, cfg.H, xq, xscale, "x")
-    o = _ptr(xperm, torch.bfloat16, ntok * cfg.K * cfg.H, "xperm")
-    _on_device(plan.route, xq, xscale, xperm)
-    _check(load().moe_dispatch_q8(ctypes.byref(cfg), plan.c, *kept, o, _stream(stream)),
-           "moe_dispatch_q8")
+    _arg(plan.route, torch.int32, ntok * cfg.K, "plan", dev)
+    _check(load().moe_dispatch_q8(ctypes.byref(cfg), plan.c,
+                                  *_kept(ntok, cfg.H, xq, xscale, "x", dev),
+                                  _arg(xperm, torch.bfloat16, ntok * cfg.K * cfg.H, "xperm", dev),
+                                  _stream(stream)), "moe_dispatch_q8")
 
 
 def moe_grouped_gemm_swiglu_q8(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, h13q, h13scale,
                                rank_begin, rank_end, workspace, stream=None):
     """cfg.Hp is the intermediate size H'; W13 rows are [H][2H'] (gate | up)."""
-    SK = cfg.S * cfg.K
+    dev = torch.cuda.current_device()
+    rows = cfg.R * cfg.S * cfg.K
     hh = cfg.H * 2 * cfg.Hp
-    args = (ctypes.byref(cfg),
-            _ptr(xperm, torch.bfloat16, cfg.R * SK * cfg.H, "xperm"),
-            _ptr(w13_home, torch.bfloat16, cfg.E * hh, "w13_home"),
-            _ptr(w13_pref, torch.bfloat16, cfg.R * cfg.B * hh, "w13_pref") if cfg.B else None,
-            _ptr(cu_seqlens, torch.int32, cfg.R * (cfg.E + cfg.B + 1), "cu_seqlens"),
-            _ptr(act, torch.bfloat16, cfg.R * SK * cfg.Hp, "act"),
-            *_kept(2 * cfg.R * SK, cfg.Hp, h13q, h13scale, "h13"),
-            int(rank_begin), int(rank_end),
-            _ptr(workspace, torch.uint8, moe_gemm_workspace_size(cfg), "workspace"))
-    _on_device(xperm, w13_home, w13_pref, cu_seqlens, act, h13q, h13scale, workspace)
-    _check(load().moe_grouped_gemm_swiglu_q8(*args, _stream(stream)),
-           "moe_grouped_gemm_swiglu_q8")
+    bf = torch.bfloat16
+    _check(load().moe_grouped_gemm_swiglu_q8(
+        ctypes.byref(cfg), _arg(xperm, bf, rows * cfg.H, "xperm", dev),
+        _arg(w13_home, bf, cfg.E * hh, "w13_home", dev),
+        _arg(w13_pref, bf, cfg.R * cfg.B * hh, "w13_pref", dev) if cfg.B else None,
+        _arg(cu_seqlens, torch.int32, cfg.R * (cfg.E + cfg.B + 1), "cu_seqlens", dev),
+        _arg(act, bf, rows * cfg.Hp, "act", dev),
+        *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13", dev), int(rank_begin), int(rank_end),
+        _arg(workspace, torch.uint8, moe_gemm_workspace_size(cfg), "workspace", dev),
+        _stream(stream)), "moe_grouped_gemm_swiglu_q8")
 
 
 def moe_swiglu_backward_q8(cfg, h13q, h13scale, dact, dh13, act=None, stream=None):
+    """dh13, and act again for the second projection's weight gradient if given."""
+    dev = torch.cuda.current_device()
     rows = cfg.R * cfg.S * cfg.K
-    args = (ctypes.byref(cfg), *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13"),
-            _ptr(dact, torch.bfloat16, rows * cfg.Hp, "dact"),
-            _ptr(dh13, torch.bfloat16, rows * 2 * cfg.Hp, "dh13"),
-            _ptr(act, torch.bfloat16, rows * cfg.Hp, "act"))
-    _on_device(h13q, h13scale, dact, dh13, act)
-    _check(load().moe_swiglu_backward_q8(*args, _stream(stream)), "moe_swiglu_backward_q8")
+    bf = torch.bfloat16
+    _check(load().moe_swiglu_backward_q8(
+        ctypes.byref(cfg), *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13", dev),
+        _arg(dact, bf, rows * cfg.Hp, "dact", dev),
+        _arg(dh13, bf, rows * 2 * cfg.Hp, "dh13", dev),
+        _arg(act, bf, rows * cfg.Hp, "act", dev), _stream(stream)), "moe_swiglu_backward_q8")
 
 
 def moe_combine_backward_q8(cfg, plan, dout, yq, yscale, gates, dy, dgates, stream=None):
+    dev = torch.cuda.current_device()
     ntok = cfg.R * cfg.S
-    args = (ctypes.byref(cfg), plan.c,
-            _ptr(dout, torch.bfloat16, ntok * cfg.Hp, "dout"),
-            *_kept(ntok * cfg.K, cfg.Hp, yq, yscale, "y"),
-            _ptr(gates, torch.float32, ntok * cfg.K, "gates"),
-            _ptr(dy, torch.bfloat16, ntok * cfg.K * cfg.Hp, "dy"),
-            _ptr(dgates, torch.float32, ntok * cfg.K, "dgates"))
-    _on_device(plan.route, dout, yq, yscale, gates, dy, dgates)
-    _check(load().moe_combine_backward_q8(*args, _stream(stream)), "moe_combine_backward_q8")
+    rows = ntok * cfg.K
+    _arg(plan.route, torch.int32, rows, "plan", dev)
+    _check(load().moe_combine_backward_q8(
+        ctypes.byref(cfg), plan.c, _arg(dout, torch.bfloat16, ntok * cfg.Hp, "dout", dev),
+        *_kept(rows, cfg.Hp, yq, yscale, "y", dev),
+        _arg(gates, torch.float32, rows, "gates", dev),
+        _arg(dy, torch.bfloat16, rows * cfg.Hp, "dy", dev),
+        _arg(dgates, torch.float32, rows, "dgates", dev), _stream(stream)),
+        "moe_combine_backward_q8")

@@ -161,8 +161,11 @@ __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __
   }
 }
 
-// Backward of combine from the codes of y: one wave per token,
+// Backward of combine from the codes of y: one workgroup per token,
 //   dy[route_k] = g_k * dout[t],  dgates[t, k] = sum_h dout[t, h] * y[route_k, h].
+// Thread i takes vectors i + 256 u of the row.  The codes of KB routes are in
+// flight before the first is used; each wave sums its part of their KB dots,
+// and the four waves' parts are added in LDS, pass after pass.
 template <int CU, int KB>
 __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict__ dout,
                                                         const q8_u32x2* __restrict__ yq,
@@ -170,20 +173,19 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
                                                         const float* __restrict__ gates,
                                                         const int32_t* __restrict__ route,
                                                         u32x4* __restrict__ dy,
-                                                        float* __restrict__ dgates, int ntok,
-                                                        int K, int hv) {
-  const int t = blockIdx.x * 4 + threadIdx.x / kWave;   // whole waves leave together
-  if (t >= ntok) return;
-  const int lane = lane_id();
+                                                        float* __restrict__ dgates, int K,
+                                                        int hv) {
+  __shared__ float s_dot[4][MOE_MAX_K];
+  const int t = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
   const int sb = (hv + 3) >> 2;
   const int myroute = lane < K ? route[int64_t(t) * K + lane] : -1;
   const float mygate = lane < K ? gates[int64_t(t) * K + lane] : 0.f;
-  float mydot = 0.f;                                    // lane k: dgates[t, k]
-  for (int c0 = 0; c0 < hv; c0 += kWave * CU) {
+  float mydot = 0.f;                                    // lane k: this wave's part of k's dot
+  for (int c0 = 0; c0 < hv; c0 += 256 * CU) {
     u32x4 d[CU];
 #pragma unroll
     for (int u = 0; u < CU; ++u) {
-      const int c = c0 + u * kWave + lane;
+      const int c = c0 + u * 256 + tid;
       d[u] = c < hv ? __builtin_nontemporal_load(dout + int64_t(t) * hv + c) : u32x4{0, 0, 0, 0};
     }
     for (int k0 = 0; k0 < K; k0 += KB) {
@@ -196,7 +198,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
         const int64_t r = ok ? src : 0;
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-          const int c = c0 + u * kWave + lane;
+          const int c = c0 + u * 256 + tid;
           v[kb][u] = q8_u32x2{0, 0};
           b[kb][u] = 127;
           if (ok && c < hv) {
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
         float part = 0.f;
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-          const int c = c0 + u * kWave + lane;
+          const int c = c0 + u * 256 + tid;
           float y[8];
           q8_decode(v[kb][u], b[kb][u], y);
           u32x4 o;
@@ -231,7 +233,10 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
       }
     }
   }
-  if (lane < K) dgates[int64_t(t) * K + lane] = mydot;
+  if (lane < K) s_dot[wv][lane] = mydot;
+  __syncthreads();
+  if (tid < K)
+    dgates[int64_t(t) * K + tid] = s_dot[0][tid] + s_dot[1][tid] + s_dot[2][tid] + s_dot[3][tid];
 }
 
 // rows x width of moe_q8_store and moe_q8_load, and their grid of tiles.
@@ -348,17 +353,16 @@ extern "C" int moe_combine_backward_q8(const moe_cfg* cfg, const moe_plan* plan,
     return MOE_EINVAL;
   if (!aligned16(dout, dy) || !aligned16(yq) || !aligned16(gates, dgates)) return MOE_EINVAL;
   const int hv = cfg->Hp / 8;
-  const int cu = (hv + kWave - 1) / kWave;
-  const dim3 grid((ntok + 3) / 4), block(256);
+  const int cu = (hv + 255) / 256;                       // vectors per thread, one pass
+  const dim3 grid(ntok), block(256);
   const u32x4* ds = reinterpret_cast<const u32x4*>(dout);
   const q8_u32x2* ysrc = reinterpret_cast<const q8_u32x2*>(yq);
   u32x4* dd = reinterpret_cast<u32x4*>(dy);
 #define MOE_COMBINE_BWD(N)                                                                   \
-  hipLaunchKernelGGL((k_combine_bwd_q8<N, 4>), grid, block, 0, stream, ds, ysrc, yscale, gates, \
-                     plan->route, dd, dgates, ntok, cfg->K, hv)
+  hipLaunchKernelGGL((k_combine_bwd_q8<N, 8>), grid, block, 0, stream, ds, ysrc, yscale, gates, \
+                     plan->route, dd, dgates, cfg->K, hv)
   if (cu <= 1) MOE_COMBINE_BWD(1);
-  else if (cu <= 2) MOE_COMBINE_BWD(2);
-  else MOE_COMBINE_BWD(4);
+  else MOE_COMBINE_BWD(2);                             // larger rows take several passes
 #undef MOE_COMBINE_BWD
   return hip_status();
 }
