@@ -159,6 +159,16 @@ def _arg(t, dtype, numel, name, device):
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, device):
+    """_stream; the current stream's handle without making a Stream object (3 us)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
 def moe_strerror(code):
     return load().moe_strerror(int(code)).decode()
 
@@ -419,7 +429,7 @@ def moe_router(cfg, rcfg, logits, bias, topk_ids, gates, cu_tokens=None, counts=
         _arg(bias, torch.float32, cfg.E, "bias", dev),
         _arg(topk_ids, torch.int32, T * cfg.K, "topk_ids", dev),
         _arg(gates, torch.float32, T * cfg.K, "gates", dev),
-        *rest, _stream(stream)), "moe_router")
+        *rest, _on(stream, dev)), "moe_router")
 
 
 def moe_balance_loss(cfg, rcfg, logits, topk_ids, cu_tokens, counts, prob, loss, workspace,
@@ -432,7 +442,7 @@ def moe_balance_loss(cfg, rcfg, logits, topk_ids, cu_tokens, counts, prob, loss,
              dev),
         _arg(topk_ids, torch.int32, T * cfg.K, "topk_ids", dev),
         *_loss_args(cfg, rcfg, cu_tokens, counts, prob, loss, workspace, dev),
-        _stream(stream)), "moe_balance_loss")
+        _on(stream, dev)), "moe_balance_loss")
 
 
 def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, dloss, dlogits,
@@ -449,7 +459,7 @@ def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, 
         _arg(cu_tokens, torch.int32, n + 1, "cu_tokens", dev),
         _arg(counts, torch.int32, n * cfg.E, "counts", dev),
         _arg(dloss, torch.float32, n, "dloss", dev),
-        _arg(dlogits, dtype, T * cfg.E, "dlogits", dev), _stream(stream)), "moe_router_backward")
+        _arg(dlogits, dtype, T * cfg.E, "dlogits", dev), _on(stream, dev)), "moe_router_backward")
 
 
 def _kept(rows, width, q, scale, what, dev):
@@ -463,7 +473,7 @@ def moe_q8_store(rows, width, src, q, scale, stream=None):
     dev = torch.cuda.current_device()
     _check(load().moe_q8_store(rows, width,
                                _arg(src, torch.bfloat16, rows * width, "src", dev),
-                               *_kept(rows, width, q, scale, "q8", dev), _stream(stream)),
+                               *_kept(rows, width, q, scale, "q8", dev), _on(stream, dev)),
            "moe_q8_store")
 
 
@@ -471,7 +481,7 @@ def moe_q8_load(rows, width, q, scale, dst, stream=None):
     dev = torch.cuda.current_device()
     _check(load().moe_q8_load(rows, width, *_kept(rows, width, q, scale, "q8", dev),
                               _arg(dst, torch.bfloat16, rows * width, "dst", dev),
-                              _stream(stream)), "moe_q8_load")
+                              _on(stream, dev)), "moe_q8_load")
 
 
 def moe_dispatch_q8(cfg, plan, xq, xscale, xperm, stream=None):
@@ -481,7 +491,7 @@ def moe_dispatch_q8(cfg, plan, xq, xscale, xperm, stream=None):
     _check(load().moe_dispatch_q8(ctypes.byref(cfg), plan.c,
                                   *_kept(ntok, cfg.H, xq, xscale, "x", dev),
                                   _arg(xperm, torch.bfloat16, ntok * cfg.K * cfg.H, "xperm", dev),
-                                  _stream(stream)), "moe_dispatch_q8")
+                                  _on(stream, dev)), "moe_dispatch_q8")
 
 
 def moe_grouped_gemm_swiglu_q8(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, h13q, h13scale,
@@ -499,7 +509,7 @@ def moe_grouped_gemm_swiglu_q8(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, 
         _arg(act, bf, rows * cfg.Hp, "act", dev),
         *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13", dev), int(rank_begin), int(rank_end),
         _arg(workspace, torch.uint8, moe_gemm_workspace_size(cfg), "workspace", dev),
-        _stream(stream)), "moe_grouped_gemm_swiglu_q8")
+        _on(stream, dev)), "moe_grouped_gemm_swiglu_q8")
 
 
 def moe_swiglu_backward_q8(cfg, h13q, h13scale, dact, dh13, act=None, stream=None):
@@ -511,7 +521,7 @@ def moe_swiglu_backward_q8(cfg, h13q, h13scale, dact, dh13, act=None, stream=Non
         ctypes.byref(cfg), *_kept(2 * rows, cfg.Hp, h13q, h13scale, "h13", dev),
         _arg(dact, bf, rows * cfg.Hp, "dact", dev),
         _arg(dh13, bf, rows * 2 * cfg.Hp, "dh13", dev),
-        _arg(act, bf, rows * cfg.Hp, "act", dev), _stream(stream)), "moe_swiglu_backward_q8")
+        _arg(act, bf, rows * cfg.Hp, "act", dev), _on(stream, dev)), "moe_swiglu_backward_q8")
 
 
 def moe_combine_backward_q8(cfg, plan, dout, yq, yscale, gates, dy, dgates, stream=None):
@@ -524,5 +534,5 @@ def moe_combine_backward_q8(cfg, plan, dout, yq, yscale, gates, dy, dgates, stre
         *_kept(rows, cfg.Hp, yq, yscale, "y", dev),
         _arg(gates, torch.float32, rows, "gates", dev),
         _arg(dy, torch.bfloat16, rows * cfg.Hp, "dy", dev),
-        _arg(dgates, torch.float32, rows, "dgates", dev), _stream(stream)),
+        _arg(dgates, torch.float32, rows, "dgates", dev), _on(stream, dev)),
         "moe_combine_backward_q8")
