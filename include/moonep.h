@@ -465,14 +465,15 @@ int moe_router_workspace_size(const moe_cfg *cfg, const moe_router_cfg *rcfg, si
  * token's being z, score s = softmax(z) or s_e = 1 / (1 + e^-z_e):
  *   topk_ids[t] = the K experts of the largest z_e (bias NULL) or of
  *                 s_e + bias_e in float64, largest first, equal ones in
- *                 ascending id; K distinct experts always
+ *                 ascending id; K distinct experts always (sums that only
+ *                 float64's own rounding parts may come in either order)
  *   gates[t][k] = scale * s_id, divided by the sum of the token's K chosen
  *                 scores if renormalize.  The bias takes part in the choice
  *                 only.
  * bias [E] fp32 or NULL, topk_ids [R*S][K] int32 and gates [R*S][K] fp32 as
  * moe_plan_run and moe_combine take them.  A logit of -inf masks an expert:
- * its score is 0 and it is chosen after all others; a row of nothing else gets
- * the lowest ids and gates of 0.  A NaN logit is chosen last of all; NaN and
+ * its score is 0 and it is chosen after all others, whatever its bias; a row of
+ * nothing else gets the lowest ids and gates of 0.  A NaN logit is chosen last of all; NaN and
  * +inf pass through the sums they enter as IEEE arithmetic has it.
  *
  * Balance loss (with counts, prob and loss given; all three or none).  Tokens

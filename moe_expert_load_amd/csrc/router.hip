@@ -1,696 +1,39 @@
-// Router: expert scores to top-k ids and gates, the balance loss of every
-// sequence with its per-expert counts, and the gradient of both by the logits.
-//
-// With z one token's E logits, s = softmax(z) or 1 / (1 + e^-z):
-//   ids    the K largest z (no bias) or s + bias (in float64), equal ones in
-//          ascending id;
-//   gates  scale * s_id, or scale * s_id / (sum of the K chosen s);
-//   p      softmax(z), or s / (sum of the E s): what the loss averages.
-// A sequence q of L tokens has counts c_e, f_e = E c_e / (K L), P_e = mean p_e
-// and loss sum_e f_e P_e; f carries no gradient.
-//
-// One wave holds one token's row: lane l has experts 128 j + 2 l and
-// 128 j + 2 l + 1, so a row of even E is read as pairs, and every reduction
-// over the experts is a DPP tree.
+// Router: the join of the loss's sums, the backward kernels and the entry
+// points.  The formulas, the row layout and the forward are in router.hpp.
 #include <algorithm>
-#include <type_traits>
 
-#include "common.hpp"
-#include "host.hpp"
+#include "router.hpp"
 
 namespace moonep {
 
-constexpr int kRtThreads = 512;
-constexpr int kRtWaves = kRtThreads / kWave;
-constexpr int kRtMaxChunks = 1024;              // workgroups whose sums are joined
-constexpr int kKeyNone = -2147483647 - 1;       // below every key: taken, or past E
-
-struct RouterArgs {
-  const void* logits;
-  const float* bias;
-  int32_t* ids;                  // written when selecting, read otherwise
-  float* gates;
-  const int32_t* cu;             // [nseq + 1], or null: one sequence of all tokens
-  float* part_p;                 // [chunks + nseq][E] sums of p
-  int32_t* part_c;               // [chunks + nseq][E] counts
-  const float* dgates;
-  const int32_t* counts;
-  const float* dloss;
-  void* dlogits;
-  int32_t T, E, K, nseq, chunk, score, renorm;
-  float scale;
-};
-
-__device__ __forceinline__ int expert_of(int i) {
-  return ((i >> 1) << 7) + 2 * lane_id() + (i & 1);
-}
-
-// Two fp32 values as packed bf16, rounded to nearest even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
-// One logit, at any alignment.
-template <bool BF16>
-__device__ __forceinline__ float logit_at(const void* z, int64_t i) {
-  if constexpr (BF16) return bf16_lo(reinterpret_cast<const uint16_t*>(z)[i]);
-  else return reinterpret_cast<const float*>(z)[i];
-}
-
-// A token's row as loaded: P / 2 pairs per lane.  FULL: E == 64 P, every lane
-// holds P experts and nothing is masked.
-template <int P, bool BF16>
-struct Row {
-  uint32_t w[BF16 ? P / 2 : P];
-};
-
-template <int P, bool BF16, bool FULL>
-__device__ __forceinline__ void load_row(const void* z, int64_t t, int E, Row<P, BF16>& r) {
-  constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;     // -inf past E
-  const int64_t at = t * E;
-#pragma unroll
-  for (int i = 0; i < P; i += 2) {
-    const int e = expert_of(i);
-    if constexpr (BF16) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(z) + at;
-      if (FULL || (E & 1) == 0) {
-        r.w[i / 2] = kNone;
-        if (FULL || e < E) r.w[i / 2] = *reinterpret_cast<const uint32_t*>(p + e);
-      } else {
-        uint32_t lo = 0xff80u, hi = 0xff80u;
-        if (e < E) lo = p[e];
-        if (e + 1 < E) hi = p[e + 1];
-        r.w[i / 2] = lo | (hi << 16);
-      }
-    } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(z) + at;
-      if (FULL || (E & 1) == 0) {
-        r.w[i] = r.w[i + 1] = kNone;
-        if (FULL || e < E) {
-          const uint2 v = *reinterpret_cast<const uint2*>(p + e);
-          r.w[i] = v.x;
-          r.w[i + 1] = v.y;
-        }
-      } else {
-        r.w[i] = e < E ? p[e] : kNone;
-        r.w[i + 1] = e + 1 < E ? p[e + 1] : kNone;
-      }
-    }
-  }
-}
-
-template <int P, bool BF16>
-__device__ __forceinline__ void unpack_row(const Row<P, BF16>& r, float (&v)[P]) {
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    if constexpr (BF16) v[i] = (i & 1) ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
-    else v[i] = __uint_as_float(r.w[i]);
-  }
-}
-
-// Order of floats as order of ints: -0 equals +0, NaN comes below -inf.
-__device__ __forceinline__ int order_key(float f) {
-  const int b = __float_as_int(f + 0.f);
-  return f != f ? kKeyNone + 1 : b ^ ((b >> 31) & 0x7fffffff);
-}
-
-__device__ __forceinline__ float key_value(int k) {
-  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
-}
-
-__device__ __forceinline__ uint64_t ballot(bool b) { return __builtin_amdgcn_ballot_w64(b); }
-
-// order_key of the largest of the 64 lanes' values; NaN is passed over.
-__device__ __forceinline__ int wave_max_key(float v) {
-  return wave_max(v != v ? kKeyNone : order_key(v));
-}
-
-// That value, -inf if there is none.
-__device__ __forceinline__ float wave_max_f(float v) {
-  const int k = wave_max_key(v);
-  return k == kKeyNone ? -INFINITY : key_value(k);
-}
-
-template <int P>
-__device__ __forceinline__ float lane_max(const float (&v)[P]) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < P; ++i) m = fmaxf(m, v[i]);
-  return m;
-}
-
-__device__ __forceinline__ double wave_sum_d(double v) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
-}
-
-__device__ __forceinline__ double lane_bcast_d(double v, int l) {
-  const int64_t b = __double_as_longlong(v);
-  const uint32_t lo = (uint32_t)wave_bcast((int)b, l);
-  const uint32_t hi = (uint32_t)wave_bcast((int)(b >> 32), l);
-  return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
-}
-
-__device__ __forceinline__ float exp_f(float x) {
-  return __builtin_amdgcn_exp2f(x * 1.44269504f);
-}
-
-// sigmoid(z) and 1 - sigmoid(z), neither by cancellation; NaN stays NaN.
-__device__ __forceinline__ float sigmoid_f(float z, float& co) {
-  const float t = exp_f(-fabsf(z));
-  const float r = __builtin_amdgcn_rcpf(1.f + t), q = t * r;
-  co = z >= 0.f ? q : r;
-  return z >= 0.f ? r : q;
-}
-
-__device__ __forceinline__ float sigmoid_f(float z) {
-  float co;
-  return sigmoid_f(z, co);
-}
-
-// Below this logit a sigmoid is e^z to fp32's last bit, and ratios of scores
-// are taken from e^(z - max) so that they survive the scores' underflow.
-constexpr float kDeep = -60.f;
-
-// Sums of exponentials in this range are taken as they are: the largest logit
-// is then between -15 and 13, so nothing overflows or underflows, and the
-// exponentials' errors are those of arguments of at most 15.  Other sums
-// (far logits, a masked row's 0, NaN) are taken again from z - max.
-constexpr float kPlainLo = 0x1p-10f, kPlainHi = 0x1p18f;
-// The same for sums of sigmoids: none of their terms that count has underflowed.
-constexpr float kSigmoidLo = 0x1p-60f;
-
-__device__ __forceinline__ float recip(float sum) {          // 0 for an empty sum
-  return sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
-}
-
-// Unnormalised shares p of token t in v (co: 1 - s for sigmoids) and their
-// factor, from its logits z.  The scores of a softmax are e^(z - shift) times
-// that factor.  A row whose every logit is -inf has p = 0.
-template <int P, bool BF16, bool FULL, bool SOFT, bool CO>
-__device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, const float (&z)[P],
-                                            float (&v)[P], float (&co)[P], float& shift) {
-  float sum = 0.f;
-  shift = 0.f;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    if constexpr (SOFT) {
-      v[i] = exp_f(z[i]);
-    } else {
-      float c;
-      v[i] = sigmoid_f(z[i], c);
-      if constexpr (CO) co[i] = c;
-    }
-    sum += v[i];
-  }
-  sum = wave_sum_f(sum);
-  if (SOFT ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo) return recip(sum);
-  // the row is loaded again, so that z need not be kept for this
-  Row<P, BF16> again;
-  load_row<P, BF16, FULL>(a.logits, t, a.E, again);
-  float x[P];
-  unpack_row<P, BF16>(again, x);
-  const float m = wave_max_f(lane_max<P>(x));
-  if (!SOFT && !(m < kDeep)) return recip(sum);              // NaN, for one
-  sum = 0.f;
-  if (m > -INFINITY) shift = m;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    v[i] = exp_f(x[i] - shift);
-    if constexpr (CO) co[i] = 1.f;                           // a deep row's 1 - s
-    sum += v[i];
-  }
-  return recip(wave_sum_f(sum));
-}
-
-// The K largest keys in order, equal ones in ascending expert; lane k returns
-// the k-th id.  key is consumed.  Any keys: K rounds of a maximum of the wave.
-template <int P>
-__device__ __forceinline__ int take_top(int (&key)[P], int K) {
-  const int lane = lane_id();
-  int mine = 0;
-  for (int k = 0; k < K; ++k) {
-    int best = key[0], bi = 0;
-#pragma unroll
-    for (int i = 1; i < P; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-      }
-    }
-    const int m = wave_max(best);
-    const int e = expert_of(bi);
-    uint64_t tied = __ballot(best == m);
-    int id = wave_bcast(e, __ffsll((unsigned long long)tied) - 1);
-    if (tied & (tied - 1)) id = -wave_max(best == m ? -e : kKeyNone);
-    if (best == m && e == id) {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (i == bi) key[i] = kKeyNone;
-    }
-    if (lane == k) mine = id;
-  }
-  return mine;
-}
-
-// A bound t such that the K largest keys are among those >= t, and few others
-// are.  `top` is the lane's largest key, `hi` the order_key of the row's.  The
-// K-th largest of the 64 lanes' largest keys is such a bound; any bound that K
-// to 3 K / 2 + 1 lanes reach is taken.  It is searched for on the scalar unit,
-// one comparison of the wave a step: from the bound of the wave's last token
-// (`probe`), whose row was much like this one, outwards by doubled steps and
-// then by halves.  -inf where there is none above it (fewer than K lanes have
-// a finite key).  The choice that follows does not depend on which is taken.
-__device__ __forceinline__ float key_bound(float top, int hi, int K, int& probe) {
-  const int most = K + (K >> 1) + 1;
-  const int low = order_key(-INFINITY);
-  const auto reach = [&](int k) { return (int)__popcll(ballot(top >= key_value(k))); };
-  const bool fresh = probe == kKeyNone;                      // no token before
-  const int step = fresh ? 1 << 20 : 1 << 18;
-  int lo = fresh ? max(hi - step, low + 1) : min(probe, hi), up = hi + 1, n = reach(lo);
-  if (n < K) {
-    for (int d = step; n < K; d <<= 1) {
-      if (d < 0 || (int64_t)lo - d <= (int64_t)low) return -INFINITY;
-      up = lo;
-      lo -= d;
-      n = reach(lo);
-    }
-  } else if (n > most) {
-    for (int d = step; d > 0 && hi - lo > d; d <<= 1) {
-      const int c = reach(lo + d);
-      if (c < K) {
-        up = lo + d;
-        break;
-      }
-      lo += d;
-      n = c;
-      if (n <= most) break;
-    }
-  }
-  while (n > most && up - lo > 1) {
-    const int mid = lo + (int)((uint32_t)(up - lo) >> 1);
-    const int c = reach(mid);
-    if (c >= K) {
-      lo = mid;
-      n = c;
-    } else {
-      up = mid;
-    }
-  }
-  probe = lo;
-  return key_value(lo);
-}
-
-// Lanes whose i-th key reaches t, for every i, and their number.
-template <int P>
-__device__ __forceinline__ int reaching(const float (&key)[P], float t, uint64_t (&m)[P]) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    m[i] = ballot(key[i] >= t);
-    n += (int)__popcll(m[i]);
-  }
-  return n;
-}
-
-// A wave's list of up to 64 keys and their experts.
-struct KeyList {
-  float key[kWave];
-  int id[kWave];
-};
-
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// Sorts the cnt <= 64 keys that m marks across the lanes, largest first, equal
-// ones in ascending expert: lane k < cnt gets the k-th key and its expert.
-// They are written to the list in ascending expert, and each lane counts the
-// keys that come before its own (a broadcast read of four keys at a time);
-// that place is where it sends them.
-template <int P>
-__device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_t (&m)[P],
-                                            int cnt, KeyList& list, float& mykey, int& mine) {
-  const int lane = lane_id();
-  int base = 0;
-#pragma unroll
-  for (int i = 0; i < P; i += 2) {
-    if ((m[i] | m[i + 1]) == 0) continue;
-    int at = base;
-    at = __builtin_amdgcn_mbcnt_lo((uint32_t)m[i], at);
-    at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i] >> 32), at);
-    at = __builtin_amdgcn_mbcnt_lo((uint32_t)m[i + 1], at);
-    at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m[i + 1] >> 32), at);
-    const bool first = __builtin_amdgcn_inverse_ballot_w64(m[i]);
-    if (first) {
-      list.key[at] = key[i];
-      list.id[at] = expert_of(i);
-    }
-    if (__builtin_amdgcn_inverse_ballot_w64(m[i + 1])) {
-      const int to = at + (first ? 1 : 0);
-      list.key[to] = key[i + 1];
-      list.id[to] = expert_of(i + 1);
-    }
-    base += (int)__popcll(m[i]) + (int)__popcll(m[i + 1]);
-  }
-  if (lane >= cnt) list.key[lane] = -INFINITY;
-  wave_lds_fence();
-  const float k = list.key[lane];
-  const int id = list.id[lane];
-  int rank = 0;
-  for (int j = 0; j < cnt; j += 4) {
-    const f32x4 o = *reinterpret_cast<const f32x4*>(list.key + j);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t later = ~uint64_t(1) << (j + q);        // lanes after j + q
-      const uint64_t before = ballot(o[q] > k) | (ballot(o[q] == k) & later);
-      rank += __builtin_amdgcn_inverse_ballot_w64(before) ? 1 : 0;
-    }
-  }
-  wave_lds_fence();                              // the list is written again
-  const int to = 4 * (lane < cnt ? rank : lane);
-  mykey = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(k)));
-  mine = __builtin_amdgcn_ds_permute(to, id);
-}
-
-// take_top through key_bound and sort_marked: the largest keys, K at least.
-// False, and nothing done, where a key is NaN or more than 64 keys reach the
-// bound.
-template <int P>
-__device__ __forceinline__ bool sort_top(const float (&key)[P], int K, int& probe, KeyList& list,
-                                         float& mykey, int& mine) {
-  uint64_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < P; i += 2) bad |= ballot(__builtin_isunordered(key[i], key[i + 1]));
-  if (bad) return false;
-  const float top = lane_max<P>(key);
-  const float t = key_bound(top, wave_max_key(top), K, probe);
-  uint64_t m[P];
-  if (t == -INFINITY) return false;
-  const int cnt = reaching<P>(key, t, m);
-  if (cnt > kWave) return false;
-  sort_marked<P>(key, m, cnt, list, mykey, mine);
-  return true;
-}
-
-// Score plus bias of one expert in float64; at: the row's first logit.
-template <bool BF16, bool SOFT>
-__device__ __forceinline__ double key64(const RouterArgs& a, int64_t at, int e, double m,
-                                        double sum) {
-  const double z = (double)logit_at<BF16>(a.logits, at + e);
-  double s;
-  if constexpr (SOFT) s = m == -INFINITY && z == z ? 0.0 : exp(z - m) / sum;
-  else s = 1.0 / (1.0 + exp(-z));
-  return s + (double)a.bias[e];
-}
-
-// Sum of a row's e^(z - m) in float64.
-template <bool BF16>
-__device__ __forceinline__ double sum64(const RouterArgs& a, int64_t at, double m) {
-  double sum = 0.0;
-#pragma unroll 1
-  for (int e = lane_id(); e < a.E; e += kWave) {
-    const double z = (double)logit_at<BF16>(a.logits, at + e);
-    if (!(m == -INFINITY && z == z)) sum += exp(z - m);
-  }
-  return wave_sum_d(sum);
-}
-
-// Orders the cnt experts `id` of lanes 0 .. cnt - 1 by float64 score plus bias.
-template <bool BF16, bool SOFT>
-__device__ __forceinline__ int order64(const RouterArgs& a, int64_t at, float mf, int cnt, int id) {
-  const int lane = lane_id();
-  const double m = (double)mf, sum = SOFT ? sum64<BF16>(a, at, m) : 1.0;
-  const double mine = lane < cnt ? key64<BF16, SOFT>(a, at, id, m, sum) : 0.0;
-  int rank = 0;
-  for (int j = 0; j < cnt; ++j) {
-    const double kj = lane_bcast_d(mine, j);
-    const int ij = wave_bcast(id, j);
-    rank += kj > mine || (kj == mine && ij < id) ? 1 : 0;
-  }
-  return __builtin_amdgcn_ds_permute(4 * (lane < cnt ? rank : lane), id);
-}
-
-// take_top on the float64 scores plus bias: the K largest, equal ones in
-// ascending expert, NaN last.  For rows that nothing else orders (NaN, more
-// than 64 keys near each other), so nothing is kept in registers between
-// rounds: the scores are computed anew.
-template <bool BF16, bool SOFT>
-__device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float mf) {
-  const int lane = lane_id();
-  const double m = (double)mf, sum = SOFT ? sum64<BF16>(a, at, m) : 1.0;
-  uint32_t taken = 0;                            // at most 32 experts a lane
-  int mine = 0;
-  for (int k = 0; k < a.K; ++k) {
-    // class of a candidate: 2 a number, 1 NaN, 0 none
-    double best = 0.0;
-    int cls = 0, id = 0x7fffffff;
-#pragma unroll 1
-    for (int i = 0, e = lane; e < a.E; ++i, e += kWave) {
-      if (taken >> i & 1) continue;
-      const double d = key64<BF16, SOFT>(a, at, e, m, sum);
-      const int c = d == d ? 2 : 1;
-      if (c > cls || (c == cls && c == 2 && d > best)) {
-        cls = c;
-        best = d;
-        id = e;
-      }
-    }
-    const int myid = id;
-    for (int o = 32; o > 0; o >>= 1) {
-      const double od = __shfl_xor(best, o, kWave);
-      const int oc = __shfl_xor(cls, o, kWave), oi = __shfl_xor(id, o, kWave);
-      const bool equal = oc == cls && (cls < 2 || od == best);
-      if (oc > cls || (oc == cls && cls == 2 && od > best) || (equal && oi < id)) {
-        best = od;
-        cls = oc;
-        id = oi;
-      }
-    }
-    if (id == myid && cls > 0) taken |= 1u << (id / kWave);
-    if (lane == k) mine = id;
-  }
-  return mine;
-}
-
-// Lane k < K: the k-th expert by score plus bias, and its logit zk.
-//
-// The order is that of float64 scores plus bias; fp32 keys give it wherever
-// neighbours among the K + 1 largest keys are further apart than two keys'
-// errors.  With h = 2^-24 a key is off by
-//   sigmoid  s (1 - s) |z| 2.2 h + 2.5 ulp of s  <=  1.4e-8 + 3e-7,
-//   softmax  s (|z - shift| 2.2 h + the sum's relative error), where
-//            s |z - max| <= 0.37 p_max and the sum's error is at most
-//            (2.2 ln E + 48 + 33) h:  <= 8e-6 p_max,
-// and by h |key| from the addition.  Other rows list every key that may be
-// among the K largest, at most 64, and order those in float64, a lane each.
-template <int P, bool BF16, bool SOFT>
-__device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, float m,
-                                             const float (&s)[P], const float (&bias)[P],
-                                             float inv, float shift, int& probe, KeyList& list,
-                                             float& zk) {
-  const int lane = lane_id();
-  const int64_t at = t * a.E;
-  const int n = a.K < a.E ? a.K + 1 : a.K;
-  float key[P], lk = 0.f;
-  int id = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) key[i] = fmaf(s[i], inv, bias[i]);
-  bool listed = n <= kWave && sort_top<P>(key, n, probe, list, lk, id);
-  if (listed) {
-    const float err = SOFT ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
-    const float ko = __shfl_down(lk, 1, kWave);
-    const bool apart = lk - ko > 2.f * err + 1.2e-7f * (fabsf(lk) + fabsf(ko));
-    if (ballot(lane < n - 1 && !apart)) {
-      const float last = __int_as_float(wave_bcast(__float_as_int(lk), a.K - 1));
-      const float reach = last - (2.f * err + 2.4e-7f * fabsf(last) + 1e-12f);
-      uint64_t in[P];
-      const int cnt = reaching<P>(key, reach, in);
-      listed = reach > -INFINITY && cnt <= kWave;
-      if (listed) {
-        sort_marked<P>(key, in, cnt, list, lk, id);
-        id = order64<BF16, SOFT>(a, at, m, cnt, id);
-      }
-    }
-  }
-  if (!listed) id = take_top64<BF16, SOFT>(a, at, m);
-  zk = logit_at<BF16>(a.logits, at + (lane < a.K ? id : 0));
-  return id;
-}
-
-// Lane k < K: the k-th expert by logit, and its logit zk.
-template <int P, bool BF16>
-__device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
-                                      int& probe, KeyList& list, float& zk) {
-  int id = 0;
-  if (sort_top<P>(z, a.K, probe, list, zk, id)) return id;
-  int key[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
-  id = take_top<P>(key, a.K);
-  zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
-  return id;
-}
-
-// Lane k < K (`on`): the gate of the chosen logit zk, over scale.
-template <bool SOFT>
-__device__ __forceinline__ float gate_share(float zk, bool on, bool renorm, float shift,
-                                            float inv) {
-  if (!renorm) {
-    if (!on) return 0.f;
-    return SOFT ? exp_f(zk - shift) * inv : sigmoid_f(zk);
-  }
-  float s = on ? SOFT ? exp_f(zk) : sigmoid_f(zk) : 0.f;
-  float sum = wave_sum_f(s);
-  const bool plain = SOFT ? sum >= kPlainLo && sum <= kPlainHi : sum >= kSigmoidLo;
-  if (!plain) {
-    const float mk = wave_max_f(on ? zk : -INFINITY);
-    if (SOFT || mk < kDeep) {
-      s = on ? exp_f(mk > -INFINITY ? zk - mk : zk) : 0.f;
-      sum = wave_sum_f(s);
-    }
-  }
-  return s * recip(sum);
-}
-
-// The sequence that holds token t (the last one with cu[s] <= t), or -1, and
-// where its tokens, or those of no sequence, end.  The lanes look at 64 places
-// of cu at once: up to 63 sequences take one load instead of a chain of them.
-__device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end) {
-  end = a.T;
-  if (!a.cu) return 0;
-  int lo = -1, hi = a.nseq + 1;                   // cu[lo] <= t < cu[hi], as if cu[hi] = inf
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64;
-    const int at = lo + (lane_id() + 1) * step;   // below 2^21 + 64 * 2^14
-    const bool in = at < hi;
-    const int c = in ? a.cu[at] : 0;
-    const int n = (int)__popcll(ballot(in && c <= t));
-    lo += n * step;
-    hi = min(hi, lo + step);
-  }
-  lo = min(lo, a.nseq);
-  if (lo >= a.nseq) return -1;                    // behind the last sequence
-  end = max(t + 1, min(a.cu[lo + 1], a.T));
-  return lo;                                      // -1: before the first sequence
-}
-
-// ---------------------------------------------------------------------------
-// Forward.  A workgroup owns `chunk` consecutive tokens, its waves take them in
-// turn, each loading its next row before it works on the present one.  Where
-// the loss is wanted, each wave keeps the sums of p in registers and the
-// workgroup the counts in LDS; both go to row (workgroup + sequence) of the
-// workspace when the sequence or the chunk ends.  Along the tokens either
-// number grows, so no two pieces share a row.
-// ---------------------------------------------------------------------------
-template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
-__global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
-  extern __shared__ float lds[];                  // [waves][E] sums, [E] counts
-  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int E = a.E, K = a.K;
-  __shared__ __attribute__((aligned(16))) KeyList lists[SELECT ? kRtWaves : 1];
-  KeyList& list = lists[SELECT ? wv : 0];
-  int probe = kKeyNone;
-  int* cnt = reinterpret_cast<int*>(lds + kRtWaves * E);
-  const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-  float acc[P], bias[P];
-  if constexpr (BIAS) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) bias[i] = expert_of(i) < E ? a.bias[expert_of(i)] : -INFINITY;
-  }
-  for (int lo = t0; lo < t1;) {
-    int hi = t1, seq = -1;
-    if constexpr (STATS) {
-      seq = sequence_of(a, lo, hi);
-      hi = min(hi, t1);
-#pragma unroll
-      for (int i = 0; i < P; ++i) acc[i] = 0.f;
-      for (int e = threadIdx.x; e < E; e += kRtThreads) cnt[e] = 0;
-      __syncthreads();
-    }
-    if (SELECT || seq >= 0) {
-      Row<P, BF16> next;
-      if (lo + wv < hi) load_row<P, BF16, FULL>(a.logits, lo + wv, E, next);
-      for (int t = lo + wv; t < hi; t += kRtWaves) {
-        float z[P], v[P], co[P];
-        unpack_row<P, BF16>(next, z);
-        if (t + kRtWaves < hi) load_row<P, BF16, FULL>(a.logits, t + kRtWaves, E, next);
-        int id = -1;
-        if constexpr (!SELECT) {
-          if (lane < K) id = a.ids[int64_t(t) * K + lane];
-        }
-        float inv = 1.f, shift = 0.f;
-        if (STATS || (SELECT && SOFT && (BIAS || !a.renorm)))
-          inv = row_shares<P, BF16, FULL, SOFT, false>(a, t, z, v, co, shift);
-        if constexpr (STATS) {
-          if (seq >= 0) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-          }
-        }
-        if constexpr (SELECT) {
-          float zk;
-          if constexpr (BIAS) {
-            float m = 0.f;
-            if constexpr (SOFT) m = wave_max_f(lane_max<P>(z));
-            if (!SOFT && (!STATS || shift != 0.f)) {      // v holds no sigmoids
-#pragma unroll
-              for (int i = 0; i < P; ++i) v[i] = sigmoid_f(z[i]);
-            }
-            id = choose_biased<P, BF16, SOFT>(a, t, m, v, bias, SOFT ? inv : 1.f, shift, probe,
-                                              list, zk);
-          } else {
-            id = choose<P, BF16>(a, t, z, probe, list, zk);
-          }
-          const bool on = lane < K;
-          const float w = gate_share<SOFT>(zk, on, a.renorm, shift, inv);
-          if (on) {
-            a.ids[int64_t(t) * K + lane] = id;
-            a.gates[int64_t(t) * K + lane] = a.scale * w;
-          }
-        }
-        if constexpr (STATS) {
-          if (seq >= 0 && lane < K && (unsigned)id < (unsigned)E) atomicAdd(&cnt[id], 1);
-        }
-      }
-    }
-    if constexpr (STATS) {
-      if (seq >= 0) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int e = expert_of(i);
-          if (FULL || e < E) lds[wv * E + e] = acc[i];
-        }
-      }
-      __syncthreads();
-      if (seq >= 0) {
-        const int64_t row = int64_t(blockIdx.x + seq) * E;
-        for (int e = threadIdx.x; e < E; e += kRtThreads) {
-          float s = 0.f;
-#pragma unroll
-          for (int w = 0; w < kRtWaves; ++w) s += lds[w * E + e];
-          a.part_p[row + e] = s;
-          a.part_c[row + e] = cnt[e];
-        }
-      }
-      __syncthreads();                            // cnt is cleared next
-    }
-    lo = hi;
-  }
-}
-
-// Joins a sequence's rows, in the order of its chunks, into counts and P, and
-// the loss where one workgroup has all experts.  A workgroup takes `ns` slices
-// of 64 experts of one sequence; its 16 waves are 16 / ns groups that take the
-// rows in turn.
+// Joins a sequence's rows into counts, P and the loss, in a fixed order.
+// k_router_join<true>: one workgroup has all `ns` slices of 64 experts of a
+// sequence and writes the results.  k_router_join<false>: a workgroup has one
+// slice and one of gridDim.z parts of the rows, and writes sums that
+// k_router_total adds up.  Its 16 waves are 16 / ns groups that take the rows in
+// turn, eight loads in flight each.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinWaves = kJoinThreads / kWave;
-constexpr int kJoinLoads = 16;                    // rows a wave has in flight
 
+template <int N>
+__device__ __forceinline__ void join_rows(const RouterArgs& a, int64_t at, int64_t stride, int n,
+                                          double& p, int& c) {
+  float fp[N];
+  int fc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {                   // all loads go out before the first sum
+    const int64_t x = at + min(j, n - 1) * stride;
+    fp[j] = a.part_p[x];
+    fc[j] = a.part_c[x];
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    p += j < n ? (double)fp[j] : 0.0;
+    c += j < n ? fc[j] : 0;
+  }
+}
+
+template <bool ONE>
 __global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int chunks, int ns,
                                                               int32_t* counts, float* prob,
                                                               float* loss) {
@@ -700,26 +43,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int 
   const int groups = kJoinWaves / ns, slice = wv % ns, group = wv / ns;
   const int lo = a.cu ? max(0, min(a.cu[seq], a.T)) : 0;
   const int hi = a.cu ? max(lo, min(a.cu[seq + 1], a.T)) : a.T;
-  const int c0 = hi > lo ? lo / a.chunk : 0, c1 = hi > lo ? min((hi - 1) / a.chunk + 1, chunks) : 0;
+  int c0 = hi > lo ? lo / a.chunk : 0, c1 = hi > lo ? min((hi - 1) / a.chunk + 1, chunks) : 0;
+  if constexpr (!ONE) {
+    const int part = (c1 - c0 + (int)gridDim.z - 1) / (int)gridDim.z;
+    c0 += (int)blockIdx.z * part;
+    c1 = min(c1, c0 + part);
+  }
   const int e = (blockIdx.y * ns + slice) * kWave + lane;
   double p = 0.0;
   int c = 0;
   if (e < a.E && group < groups) {
-    for (int r0 = c0 + group; r0 < c1; r0 += kJoinLoads * groups) {
-      float fp[kJoinLoads];
-      int fc[kJoinLoads];
-#pragma unroll
-      for (int j = 0; j < kJoinLoads; ++j) {      // all loads go out before the first sum
-        const int64_t at = int64_t(min(r0 + j * groups, c1 - 1) + seq) * a.E + e;
-        fp[j] = a.part_p[at];
-        fc[j] = a.part_c[at];
-      }
-#pragma unroll
-      for (int j = 0; j < kJoinLoads; ++j) {
-        const bool in = r0 + j * groups < c1;
-        p += in ? (double)fp[j] : 0.0;
-        c += in ? fc[j] : 0;
-      }
+    const int64_t stride = int64_t(groups) * a.E;
+    for (int r = c0 + group; r < c1; r += 8 * groups) {
+      const int64_t at = int64_t(r + seq) * a.E + e;
+      const int n = (c1 - r + groups - 1) / groups;
+      if (n > 2) join_rows<8>(a, at, stride, n, p, c);
+      else join_rows<2>(a, at, stride, n, p, c);
     }
   }
   s_p[wv][lane] = p;
@@ -731,39 +70,59 @@ __global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int 
       p += s_p[g * ns + slice][lane];
       c += s_c[g * ns + slice][lane];
     }
-    const float mean = hi > lo ? (float)(p / (double)(hi - lo)) : 0.f;
-    counts[int64_t(seq) * a.E + e] = c;
-    prob[int64_t(seq) * a.E + e] = mean;
-    f = (double)c * (double)mean;
+    if constexpr (ONE) {
+      const float mean = hi > lo ? (float)(p / (double)(hi - lo)) : 0.f;
+      counts[int64_t(seq) * a.E + e] = c;
+      prob[int64_t(seq) * a.E + e] = mean;
+      f = (double)c * (double)mean;
+    } else {
+      const int64_t at = (int64_t(seq) * gridDim.z + blockIdx.z) * a.E + e;
+      a.sum_p[at] = p;
+      a.sum_c[at] = c;
+    }
   }
-  if (gridDim.y > 1) return;                      // k_router_loss follows
-  __syncthreads();
-  f = wave_sum_d(f);
-  if (lane == 0) s_p[wv][0] = f;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < ns; ++w) f += s_p[w][0];
-    loss[seq] = hi > lo ? (float)(f * a.E / ((double)a.K * (hi - lo))) : 0.f;
+  if constexpr (ONE) {
+    __syncthreads();
+    f = wave_sum_d(f);
+    if (lane == 0) s_p[wv][0] = f;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < ns; ++w) f += s_p[w][0];
+      loss[seq] = hi > lo ? (float)(f * a.E / ((double)a.K * (hi - lo))) : 0.f;
+    }
   }
 }
 
-// The loss of a sequence from its counts and P.
-constexpr int kLossThreads = 512;
+// A sequence's results from its Z parts' sums.
+constexpr int kTotalThreads = 512;
 
-__global__ __launch_bounds__(kLossThreads) void k_router_loss(RouterArgs a, const int32_t* counts,
-                                                              const float* prob, float* loss) {
-  __shared__ double part[kLossThreads / kWave];
+template <int Z>
+__global__ __launch_bounds__(kTotalThreads) void k_router_total(RouterArgs a, int32_t* counts,
+                                                                float* prob, float* loss) {
+  __shared__ double s_f[kTotalThreads / kWave];
   const int seq = blockIdx.x;
   const int lo = a.cu ? max(0, min(a.cu[seq], a.T)) : 0;
   const int hi = a.cu ? max(lo, min(a.cu[seq + 1], a.T)) : a.T;
   double f = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kLossThreads)
-    f += (double)counts[int64_t(seq) * a.E + e] * (double)prob[int64_t(seq) * a.E + e];
+  for (int e = threadIdx.x; e < a.E; e += kTotalThreads) {
+    const int64_t at = int64_t(seq) * Z * a.E + e;
+    double p = 0.0;
+    int c = 0;
+#pragma unroll
+    for (int z = 0; z < Z; ++z) {
+      p += a.sum_p[at + int64_t(z) * a.E];
+      c += a.sum_c[at + int64_t(z) * a.E];
+    }
+    const float mean = hi > lo ? (float)(p / (double)(hi - lo)) : 0.f;
+    counts[int64_t(seq) * a.E + e] = c;
+    prob[int64_t(seq) * a.E + e] = mean;
+    f += (double)c * (double)mean;
+  }
   f = wave_sum_d(f);
-  if (lane_id() == 0) part[threadIdx.x / kWave] = f;
+  if (lane_id() == 0) s_f[threadIdx.x / kWave] = f;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kLossThreads / kWave; ++w) f += part[w];
+    for (int w = 1; w < kTotalThreads / kWave; ++w) f += s_f[w];
     loss[seq] = hi > lo ? (float)(f * a.E / ((double)a.K * (hi - lo))) : 0.f;
   }
 }
@@ -782,7 +141,7 @@ __global__ __launch_bounds__(kLossThreads) void k_router_loss(RouterArgs a, cons
 // A gradient of renormalised gates alone reads only the K chosen logits.
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT>
-__global__ __launch_bounds__(kRtThreads) void k_router_bwd(RouterArgs a) {
+__global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router_bwd(RouterArgs a) {
   extern __shared__ float lds[];                  // [waves][64 P]
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
@@ -927,7 +286,16 @@ inline int stats_chunks(int T) { return T > 0 ? (T + stats_chunk(T) - 1) / stats
 // Rows times slices of experts up to which one workgroup joins a sequence.
 constexpr int kJoinOne = 512;
 
+// Parts into which a sequence's rows are joined first: several where a sequence
+// has 256 rows or more on average (fewer leave a wave one round of loads).
+constexpr int kJoinParts = 8;
+inline int join_parts(int T, int nseq) {
+  return stats_chunks(T) >= int64_t(256) * nseq ? kJoinParts : 1;
+}
+
+// Workspace: joined sums, then the rows' sums, then both counts.
 inline size_t part_rows(int T, int nseq) { return size_t(stats_chunks(T)) + size_t(nseq); }
+inline size_t sum_rows(int T, int nseq) { return size_t(nseq) * join_parts(T, nseq); }
 
 inline int check_router(const moe_cfg* c, const moe_router_cfg* r) {
   const int rc = check_cfg(c);
@@ -938,31 +306,6 @@ inline int check_router(const moe_cfg* c, const moe_router_cfg* r) {
     return MOE_EINVAL;
   if (r->nseq > MOE_MAX_NSEQ) return MOE_ELIMIT;
   return MOE_OK;
-}
-
-// Calls f with the registers per lane of a row of E experts, the type, and
-// whether the row fills all lanes.
-template <typename F>
-inline int with_row(int E, bool bf16, F f) {
-  const int p = 2 * ((E + 127) / 128);
-#define MOE_ROW(N)                                                                      \
-  if (p <= N) {                                                                         \
-    constexpr std::integral_constant<int, N> n;                                         \
-    if (E == 64 * N)                                                                    \
-      return bf16 ? f(n, std::true_type(), std::true_type())                            \
-                  : f(n, std::false_type(), std::true_type());                          \
-    return bf16 ? f(n, std::true_type(), std::false_type())                             \
-                : f(n, std::false_type(), std::false_type());                           \
-  }
-  MOE_ROW(2)
-  MOE_ROW(4)
-  MOE_ROW(6)
-  MOE_ROW(8)
-  MOE_ROW(14)
-  MOE_ROW(20)
-  MOE_ROW(32)
-#undef MOE_ROW
-  return MOE_ELIMIT;
 }
 
 inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, bool select,
@@ -980,47 +323,38 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
   if (stats) {
     a.chunk = stats_chunk(a.T);
     chunks = stats_chunks(a.T);
-    a.part_p = reinterpret_cast<float*>(workspace);
-    a.part_c = reinterpret_cast<int32_t*>(a.part_p + part_rows(a.T, a.nseq) * a.E);
+    const size_t rows = part_rows(a.T, a.nseq) * a.E, sums = sum_rows(a.T, a.nseq) * a.E;
+    a.sum_p = reinterpret_cast<double*>(workspace);
+    a.part_p = reinterpret_cast<float*>(a.sum_p + sums);
+    a.part_c = reinterpret_cast<int32_t*>(a.part_p + rows);
+    a.sum_c = a.part_c + rows;
   } else {
     a.chunk = kRtWaves;
   }
   if (a.T > 0) {
     const int grid = stats ? chunks : (a.T + a.chunk - 1) / a.chunk;
-    const size_t lds = stats ? size_t(kRtWaves + 1) * a.E * 4 : 0;
-    const int rc = with_row(a.E, r->logits_bf16, [&](auto p, auto b, auto full) {
-      constexpr int P = decltype(p)::value;
-      constexpr bool BF = decltype(b)::value, FULL = decltype(full)::value;
-      const dim3 g(grid), t(kRtThreads);
-#define MOE_ROUTER(SEL, BIAS, STATS)                                                           \
-  if (a.score == MOE_SCORE_SOFTMAX)                                                            \
-    hipLaunchKernelGGL((k_router<P, BF, FULL, true, SEL, BIAS, STATS>), g, t, lds, stream, a); \
-  else                                                                                         \
-    hipLaunchKernelGGL((k_router<P, BF, FULL, false, SEL, BIAS, STATS>), g, t, lds, stream, a)
-      if (!select) {
-        MOE_ROUTER(false, false, true);
-      } else if (stats && a.bias) {
-        MOE_ROUTER(true, true, true);
-      } else if (stats) {
-        MOE_ROUTER(true, false, true);
-      } else if (a.bias) {
-        MOE_ROUTER(true, true, false);
-      } else {
-        MOE_ROUTER(true, false, false);
-      }
-#undef MOE_ROUTER
-      return hip_status();
-    });
+    const int rc = r->score == MOE_SCORE_SOFTMAX
+                       ? launch_forward<true>(a, r->logits_bf16, select, stats, grid, stream)
+                       : launch_forward<false>(a, r->logits_bf16, select, stats, grid, stream);
     if (rc != MOE_OK) return rc;
   }
   if (stats) {
     const int slices = (a.E + kWave - 1) / kWave;
-    const bool one = slices <= kJoinWaves && chunks * slices <= kJoinOne;
-    hipLaunchKernelGGL(k_router_join, dim3(a.nseq, one ? 1 : slices), dim3(kJoinThreads), 0, stream,
-                       a, chunks, one ? slices : 1, counts, prob, loss);
-    if (!one && slices > 1)
-      hipLaunchKernelGGL(k_router_loss, dim3(a.nseq), dim3(kLossThreads), 0, stream, a, counts, prob,
-                         loss);
+    const dim3 t(kJoinThreads);
+    if (slices <= kJoinWaves && chunks * slices <= kJoinOne) {
+      hipLaunchKernelGGL(k_router_join<true>, dim3(a.nseq), t, 0, stream, a, chunks, slices,
+                         counts, prob, loss);
+      return hip_status();
+    }
+    const int z = join_parts(a.T, a.nseq);
+    hipLaunchKernelGGL(k_router_join<false>, dim3(a.nseq, slices, z), t, 0, stream, a, chunks, 1,
+                       counts, prob, loss);
+    if (z > 1)
+      hipLaunchKernelGGL(k_router_total<kJoinParts>, dim3(a.nseq), dim3(kTotalThreads), 0, stream,
+                         a, counts, prob, loss);
+    else
+      hipLaunchKernelGGL(k_router_total<1>, dim3(a.nseq), dim3(kTotalThreads), 0, stream, a,
+                         counts, prob, loss);
     return hip_status();
   }
   return MOE_OK;
@@ -1035,7 +369,9 @@ extern "C" int moe_router_workspace_size(const moe_cfg* cfg, const moe_router_cf
   const int rc = check_router(cfg, rcfg);
   if (rc != MOE_OK) return rc;
   if (!bytes_out) return MOE_EINVAL;
-  *bytes_out = align256(part_rows(cfg->R * cfg->S, rcfg->nseq) * cfg->E * 8);
+  const int T = cfg->R * cfg->S;
+  *bytes_out =
+      align256((part_rows(T, rcfg->nseq) * 8 + sum_rows(T, rcfg->nseq) * 12) * cfg->E);
   return MOE_OK;
 }
 

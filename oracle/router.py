@@ -36,9 +36,12 @@ def scores(z, score):
 
 
 def choose(z, bias, K, score):
-    """The K largest of z, or of s + bias; equal ones in ascending id; NaN last."""
+    """The K largest of z, or of s + bias; equal ones in ascending id; masked ones behind,
+    NaN last."""
     z = np.asarray(z, np.float64)
-    key = z if bias is None else scores(z, score)[0] + np.asarray(bias, np.float64)
+    key = z
+    if bias is not None:                               # a logit of -inf masks its expert
+        key = np.where(z == -np.inf, -np.inf, scores(z, score)[0] + np.asarray(bias, np.float64))
     nan = np.isnan(key)
     order = np.lexsort((np.broadcast_to(np.arange(z.shape[1]), z.shape),
                         -np.where(nan, -np.inf, key), nan), axis=1)

@@ -236,11 +236,15 @@ def test_masks_ties_and_extremes(score):
     cu = np.array([0, 1, T - 2, T], np.int32)
     dg = g.standard_normal((T, K)).astype(np.float32)
     dl = g.standard_normal(3).astype(np.float32)
-    for renorm in (0, 1):
+    bias = (0.3 * g.standard_normal(E)).astype(np.float32)
+    bias[3], bias[4] = 50.0, -50.0
+    for renorm, b in ((0, None), (1, None), (0, bias), (1, np.zeros(E, np.float32))):
         rc = mx.make_router_cfg(score, renorm, 1.0, False, 3)
         z64 = z.astype(np.float64)
-        got = run_forward(c, rc, on_gpu(z, torch.float32), None, on_gpu(cu, torch.int32), True)
-        ids = check_forward(z64, None, got, c, rc, cu)
+        got = run_forward(c, rc, on_gpu(z, torch.float32),
+                          None if b is None else on_gpu(b, torch.float32),
+                          on_gpu(cu, torch.int32), True)
+        ids = check_forward(z64, b, got, c, rc, cu)
         assert np.isfinite(got["gates"]).all() and np.all(got["gates"][0] == 0)
         counts = O.balance(z64, ids, cu, score)[0]
         want, size = O.backward(z64, ids, score, bool(renorm), 1.0, dg, cu, counts, dl)
@@ -438,6 +442,54 @@ def test_no_tokens():
     assert not got["counts"].any() and not got["prob"].any() and not got["loss"].any()
     mx.moe_router_backward(c, rc, z, torch.empty(0, dtype=torch.int32, device="cuda"),
                            torch.empty(0, device="cuda"), None, None, None, z)
+
+
+def test_rows_of_one_wave_in_any_order():
+    """The bound that a wave's last row left behind must not matter: rows of far apart sizes
+    and signs follow each other, many more than waves."""
+    g = np.random.default_rng(29)
+    E, K, T = 128, 8, 1024 * 40
+    z = g.standard_normal((T, E)).astype(np.float32)
+    z *= (10.0 ** g.integers(-30, 31, (T, 1))).astype(np.float32)
+    z += (g.integers(-1, 2, (T, 1)) * 10.0 ** g.integers(-10, 30, (T, 1))).astype(np.float32)
+    z[g.random(T) < 0.05] = -np.inf
+    z[g.random(T) < 0.05] = 0.0
+    c = cfg_of(8, T // 8, E, K)
+    rc = mx.make_router_cfg(O.SOFTMAX, 1, 1.0, False, 1)
+    got = run_forward(c, rc, on_gpu(z, torch.float32), None, None, True)
+    assert np.array_equal(got["ids"], O.choose(z.astype(np.float64), None, K, O.SOFTMAX))
+    bias = np.zeros(E, np.float32)
+    few = slice(0, 4096)
+    c = cfg_of(8, 512, E, K)
+    for score in (O.SOFTMAX, O.SIGMOID):
+        rc = mx.make_router_cfg(score, 1, 1.0, False, 1)
+        got = run_forward(c, rc, on_gpu(z[few], torch.float32), on_gpu(bias, torch.float32), None,
+                          True)
+        want = O.choose(z[few].astype(np.float64), bias, K, score)
+        # Scores in float64 come from an exponential, a sum or 1 + x, and a division, each off
+        # by an ulp or two (2^-52): where neighbours among the K + 1 largest are nearer than
+        # 8 * 2^-52 of the score without being equal logits, float64 itself has no order, and
+        # only the chosen scores are compared.
+        s = O.scores(z[few].astype(np.float64), score)[0]
+        more = O.choose(z[few].astype(np.float64), bias, K + 1, score)
+        sk = np.take_along_axis(s, more, 1)
+        zk = np.take_along_axis(z[few], more, 1)
+        near = (sk[:, :-1] - sk[:, 1:] <= 8 * 2.0 ** -52 * sk[:, :-1]) & (zk[:, :-1] != zk[:, 1:])
+        clear = ~near.any(axis=1)
+        assert clear.mean() > 0.5
+        assert np.array_equal(got["ids"][clear], want[clear])
+        sg = np.take_along_axis(s, got["ids"], 1)
+        assert np.all(np.abs(sg - sk[:, :-1]) <= 16 * 2.0 ** -52 * sk[:, :-1])
+
+
+def test_one_device(monkeypatch):
+    c = cfg_of(1, 4, 8, 2)
+    rc = mx.make_router_cfg(O.SOFTMAX, 1)
+    z = torch.zeros((4, 8), device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        mx.moe_router(c, rc, z, None, ids, torch.zeros((4, 2), device="cuda:0"))
 
 
 def test_binding_refuses_wrong_tensors():
