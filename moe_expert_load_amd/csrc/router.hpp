@@ -330,11 +330,31 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Number of listed keys that come before key k, the one at place `cand`: larger
+// ones, and equal ones at earlier places.  The G groups of 64 / G lanes hold
+// the same candidates (cand = lane modulo the group) and look at a G-th of the
+// list each, four keys a read.
+template <int G>
+__device__ __forceinline__ int count_before(const KeyList& list, int cnt, float k) {
+  constexpr int L = kWave / G;
+  const int per = (cnt + 4 * G - 1) / (4 * G) * 4;           // places per group, G * per <= 64
+  const int first = lane_id() / L * per;
+  int ahead = lane_id() % L - first;                         // cand - place
+  int rank = 0;
+  for (int j = 0; j < per; j += 4, ahead -= 4) {
+    const f32x4 o = *reinterpret_cast<const f32x4*>(list.key + first + j);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) rank += (o[q] > k) | ((o[q] == k) & (ahead > q)) ? 1 : 0;
+  }
+  if constexpr (G == 4) rank += __shfl_xor(rank, 16, kWave);
+  if constexpr (G >= 2) rank += __shfl_xor(rank, 32, kWave);
+  return rank;
+}
+
 // Sorts the cnt <= 64 keys that m marks across the lanes, largest first, equal
 // ones in ascending expert: lane k < cnt gets the k-th key and its expert.
-// They are written to the list in ascending expert, and each lane counts the
-// keys that come before its own (a broadcast read of four keys at a time);
-// that place is where it sends them.
+// They are written to the list in ascending expert, each one's place in the
+// order is counted, and that is where its lane sends it.
 template <int P>
 __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_t (&m)[P],
                                             int cnt, KeyList& list, float& mykey, int& mine) {
@@ -362,20 +382,15 @@ __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_
   }
   if (lane >= cnt) list.key[lane] = -INFINITY;
   wave_lds_fence();
-  const float k = list.key[lane];
+  const int groups = cnt <= 16 ? 4 : cnt <= 32 ? 2 : 1;
+  const float k = list.key[lane & (kWave / groups - 1)];
   const int id = list.id[lane];
-  int rank = 0;
-  for (int j = 0; j < cnt; j += 4) {
-    const f32x4 o = *reinterpret_cast<const f32x4*>(list.key + j);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t later = ~uint64_t(1) << (j + q);        // lanes after j + q
-      const uint64_t before = ballot(o[q] > k) | (ballot(o[q] == k) & later);
-      rank += __builtin_amdgcn_inverse_ballot_w64(before) ? 1 : 0;
-    }
-  }
+  const int rank = groups == 4   ? count_before<4>(list, cnt, k)
+                   : groups == 2 ? count_before<2>(list, cnt, k)
+                                 : count_before<1>(list, cnt, k);
   wave_lds_fence();                              // the list is written again
   const int to = 4 * (lane < cnt ? rank : lane);
+  // (lanes past the first group send what they hold of the list, behind cnt)
   mykey = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(k)));
   mine = __builtin_amdgcn_ds_permute(to, id);
 }
@@ -384,12 +399,14 @@ __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_
 // False, and nothing done, where a key is NaN or more than 64 keys reach the
 // bound.
 template <int P>
-__device__ __forceinline__ bool sort_top(const float (&key)[P], int K, int& probe, KeyList& list,
-                                         float& mykey, int& mine) {
-  uint64_t bad = 0;
+__device__ __forceinline__ bool sort_top(const float (&key)[P], bool no_nan, int K, int& probe,
+                                         KeyList& list, float& mykey, int& mine) {
+  if (!no_nan) {
+    uint64_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < P; i += 2) bad |= ballot(__builtin_isunordered(key[i], key[i + 1]));
-  if (bad) return false;
+    for (int i = 0; i < P; i += 2) bad |= ballot(__builtin_isunordered(key[i], key[i + 1]));
+    if (bad) return false;
+  }
   const float top = lane_max<P>(key);
   const float t = key_bound(top, wave_max_key(top), K, probe);
   uint64_t m[P];
@@ -502,7 +519,7 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, flo
   const int n = a.K < a.E ? a.K + 1 : a.K;
   float lk = 0.f;
   int id = 0;
-  bool listed = n <= kWave && sort_top<P>(key, n, probe, list, lk, id);
+  bool listed = n <= kWave && sort_top<P>(key, false, n, probe, list, lk, id);
   if (listed) {
     const float err = SOFT ? 8e-6f * exp_f(m - shift) * inv : 3.2e-7f;
     const float ko = __shfl_down(lk, 1, kWave);
@@ -527,9 +544,9 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, flo
 // Lane k < K: the k-th expert by logit, and its logit zk.
 template <int P, bool BF16>
 __device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
-                                      int& probe, KeyList& list, float& zk) {
+                                      bool no_nan, int& probe, KeyList& list, float& zk) {
   int id = 0;
-  if (sort_top<P>(z, a.K, probe, list, zk, id)) return id;
+  if (sort_top<P>(z, no_nan, a.K, probe, list, zk, id)) return id;
   int key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
@@ -655,7 +672,8 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
             }
             id = choose_biased<P, BF16, SOFT>(a, t, m, v, inv, shift, probe, list, zk);
           } else {
-            id = choose<P, BF16>(a, t, z, probe, list, zk);
+            // a sum of shares that is a number has no NaN in it
+            id = choose<P, BF16>(a, t, z, STATS && inv > 0.f, probe, list, zk);
           }
           const bool on = lane < K;
           const float w = gate_share<SOFT>(zk, on, a.renorm, shift, inv);
