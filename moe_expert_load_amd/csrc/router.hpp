@@ -542,14 +542,15 @@ __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, flo
 }
 
 // Lane k < K: the k-th expert by logit, and its logit zk.
-template <int P, bool BF16>
+template <int P, bool BF16, bool FULL>
 __device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const float (&z)[P],
                                       bool no_nan, int& probe, KeyList& list, float& zk) {
   int id = 0;
   if (sort_top<P>(z, no_nan, a.K, probe, list, zk, id)) return id;
   int key[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) key[i] = expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
+  for (int i = 0; i < P; ++i)
+    key[i] = FULL || expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
   id = take_top<P>(key, a.K);
   zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
   return id;
@@ -619,7 +620,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
   float acc[P], bias[P];
   if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) bias[i] = expert_of(i) < E ? a.bias[expert_of(i)] : -INFINITY;
+    for (int i = 0; i < P; ++i) bias[i] = FULL || expert_of(i) < E ? a.bias[expert_of(i)] : -INFINITY;
   }
   for (int lo = t0; lo < t1;) {
     int hi = t1, seq = -1;
@@ -673,7 +674,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
             id = choose_biased<P, BF16, SOFT>(a, t, m, v, inv, shift, probe, list, zk);
           } else {
             // a sum of shares that is a number has no NaN in it
-            id = choose<P, BF16>(a, t, z, STATS && inv > 0.f, probe, list, zk);
+            id = choose<P, BF16, FULL>(a, t, z, STATS && inv > 0.f, probe, list, zk);
           }
           const bool on = lane < K;
           const float w = gate_share<SOFT>(zk, on, a.renorm, shift, inv);
