@@ -396,8 +396,8 @@ __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_
 }
 
 // take_top through key_bound and sort_marked: the largest keys, K at least.
-// False, and nothing done, where a key is NaN or more than 64 keys reach the
-// bound.
+// False, and nothing done, where a key is NaN, more than 64 keys reach the
+// bound, or fewer than K keys are finite.
 template <int P>
 __device__ __forceinline__ bool sort_top(const float (&key)[P], bool no_nan, int K, int& probe,
                                          KeyList& list, float& mykey, int& mine) {
@@ -408,11 +408,11 @@ __device__ __forceinline__ bool sort_top(const float (&key)[P], bool no_nan, int
     if (bad) return false;
   }
   const float top = lane_max<P>(key);
-  const float t = key_bound(top, wave_max_key(top), K, probe);
+  float t = key_bound(top, wave_max_key(top), K, probe);
+  if (t == -INFINITY) t = -3.402823466e38f;      // every finite key: 64 experts, or a mask
   uint64_t m[P];
-  if (t == -INFINITY) return false;
   const int cnt = reaching<P>(key, t, m);
-  if (cnt > kWave) return false;
+  if (cnt < K || cnt > kWave) return false;
   sort_marked<P>(key, m, cnt, list, mykey, mine);
   return true;
 }
