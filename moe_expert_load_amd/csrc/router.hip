@@ -276,12 +276,14 @@ __global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router
   }
 }
 
-// Tokens per workgroup and workgroups of a forward call that keeps sums.
-inline int stats_chunk(int T) {
-  const int c = (T + kRtMaxChunks - 1) / kRtMaxChunks;
-  return c > kRtWaves ? c : kRtWaves;
+// Tokens per workgroup of a forward call that keeps sums in at most `most`
+// workgroups: whole rounds of its waves.
+inline int stats_chunk(int T, int most) {
+  const int rounds = (T + most * kRtWaves - 1) / (most * kRtWaves);
+  return kRtWaves * (rounds > 1 ? rounds : 1);
 }
-inline int stats_chunks(int T) { return T > 0 ? (T + stats_chunk(T) - 1) / stats_chunk(T) : 0; }
+inline int chunks_of(int T, int chunk) { return (T + chunk - 1) / chunk; }
+inline int max_chunks(int T) { return chunks_of(T, stats_chunk(T, kRtMaxChunks)); }
 
 // Rows times slices of experts up to which one workgroup joins a sequence.
 constexpr int kJoinOne = 512;
@@ -290,11 +292,11 @@ constexpr int kJoinOne = 512;
 // has 256 rows or more on average (fewer leave a wave one round of loads).
 constexpr int kJoinParts = 8;
 inline int join_parts(int T, int nseq) {
-  return stats_chunks(T) >= int64_t(256) * nseq ? kJoinParts : 1;
+  return max_chunks(T) >= int64_t(256) * nseq ? kJoinParts : 1;
 }
 
 // Workspace: joined sums, then the rows' sums, then both counts.
-inline size_t part_rows(int T, int nseq) { return size_t(stats_chunks(T)) + size_t(nseq); }
+inline size_t part_rows(int T, int nseq) { return size_t(max_chunks(T)) + size_t(nseq); }
 inline size_t sum_rows(int T, int nseq) { return size_t(nseq) * join_parts(T, nseq); }
 
 inline int check_router(const moe_cfg* c, const moe_router_cfg* r) {
@@ -321,8 +323,8 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
   a.scale = r->scale;
   int chunks = 0;
   if (stats) {
-    a.chunk = stats_chunk(a.T);
-    chunks = stats_chunks(a.T);
+    a.chunk = stats_chunk(a.T, select ? kRtSelectChunks : kRtMaxChunks);
+    chunks = chunks_of(a.T, a.chunk);
     const size_t rows = part_rows(a.T, a.nseq) * a.E, sums = sum_rows(a.T, a.nseq) * a.E;
     a.sum_p = reinterpret_cast<double*>(workspace);
     a.part_p = reinterpret_cast<float*>(a.sum_p + sums);

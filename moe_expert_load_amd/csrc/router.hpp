@@ -23,7 +23,12 @@ namespace moonep {
 
 constexpr int kRtThreads = 512;
 constexpr int kRtWaves = kRtThreads / kWave;
-constexpr int kRtMaxChunks = 1024;              // workgroups whose sums are joined
+// Workgroups whose sums are joined, at most; and how many a call that chooses
+// makes of its tokens: its registers leave two workgroups a CU, and a second
+// round of workgroups costs more than it evens out (65,536 tokens of 384
+// experts: 50.3 us in 512 workgroups, 55.9 in 1,024).
+constexpr int kRtMaxChunks = 1024;
+constexpr int kRtSelectChunks = 512;
 constexpr int kKeyNone = -2147483647 - 1;       // below every key: taken, or past E
 
 struct RouterArgs {
@@ -608,7 +613,7 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // number grows, so no two pieces share a row.
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
-__global__ __launch_bounds__(kRtThreads) void k_router(RouterArgs a) {
+__global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterArgs a) {
   extern __shared__ float lds[];                  // [waves][E] sums, [E] counts
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;

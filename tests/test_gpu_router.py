@@ -12,8 +12,8 @@ Tolerances, from the arithmetic, with h = 2^-24 (half an fp32 step, relative):
   a lane and 6 across lanes, and the reciprocal and products that follow, 4
   more: a share is off by rel = (5 X + 2 + 32 + 6 + 8) h at most;
 * what fp32 cannot hold (scores below 2^-126) is 2^-126 absolute;
-* the sums over a sequence: one wave adds at most chunk / 4 tokens, then 4
-  waves; the join is float64.  chunk = ceil(T / 1024);
+* the sums over a sequence: one wave adds at most chunk / 8 tokens, then 8
+  waves; the join is float64.  chunk = 8 ceil(T / 4096) at most;
 * the gradient is a sum of terms whose magnitudes the oracle adds up (size);
   each is a product of up to 3 rounded shares and 6 roundings, and its mean
   over experts adds 40 more: (3 rel + 48 h) size.  A bf16 result adds half a
@@ -141,8 +141,8 @@ def check_forward(z, bias, got, c, rc, cu):
 
 def check_sums(z, got, c, rc, prob, loss):
     T = c.R * c.S
-    chunk = -(-T // 1024)
-    r = float(rel_of(z, rc.score).max(initial=0)) + (chunk / 4 + 8) * h
+    chunk = 8 * -(-T // 4096)
+    r = float(rel_of(z, rc.score).max(initial=0)) + (chunk / 8 + 8) * h
     assert np.all(np.abs(got["prob"] - prob) <= r * prob + TINY_ABS)
     assert np.all(np.abs(got["loss"] - loss) <= (r + 8 * h) * loss + TINY_ABS)
 

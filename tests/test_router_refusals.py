@@ -92,7 +92,7 @@ def test_workspace_size_covers_every_piece():
     # chunks + sequences rows of E sums and E counts, and the joined double sums and counts
     for T, E, n in ((1, 8, 1), (1024, 384, 5), (1025, 384, 1), (65536, 896, 64), (65536, 384, 1)):
         c = mx.make_cfg(1, T, E, 1, 8, 8, 0, mx.MODE_INFER)
-        chunk = max(8, -(-T // 1024))
+        chunk = 8 * max(1, -(-T // 8192))
         chunks = -(-T // chunk)
         parts = 8 if chunks >= 256 * n else 1
         need = (chunks + n) * E * 8 + n * parts * E * 12
