@@ -66,9 +66,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_router_join(RouterArgs a, int 
   __syncthreads();
   double f = 0.0;
   if (group == 0 && e < a.E) {
-    for (int g = 1; g < groups; ++g) {
-      p += s_p[g * ns + slice][lane];
-      c += s_c[g * ns + slice][lane];
+#pragma unroll
+    for (int g = 1; g < kJoinWaves; ++g) {        // LDS reads without a wait between them
+      const int w = min(g * ns + slice, kJoinWaves - 1);
+      const double gp = s_p[w][lane];
+      const int gc = s_c[w][lane];
+      p += g < groups ? gp : 0.0;
+      c += g < groups ? gc : 0;
     }
     if constexpr (ONE) {
       const float mean = hi > lo ? (float)(p / (double)(hi - lo)) : 0.f;
