@@ -3,6 +3,7 @@
 // backward of the SwiGLU activation and of combine from the codes of h13 and
 // of y.  The format is in q8.hpp.  All of them stream: what they cost is the
 // bytes of their tensors.
+#include "convert.hpp"
 #include "host.hpp"
 #include "q8.hpp"
 
@@ -153,9 +154,9 @@ __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __
           dg[i] = d * up * s * (1.f + gate * (1.f - s));
           a[i] = gs1 * up;
         }
-        og[q] = pack_bf16x2(dg[0], dg[1]);
-        ou[q] = pack_bf16x2(du[0], du[1]);
-        oa[q] = pack_bf16x2(a[0], a[1]);
+        og[q] = cvt_bf16x2(dg[0], dg[1]);
+        ou[q] = cvt_bf16x2(du[0], du[1]);
+        oa[q] = cvt_bf16x2(a[0], a[1]);
       }
       dh13[r * 2 * hv + c] = og;
       dh13[r * 2 * hv + hv + c] = ou;

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "convert.hpp"
 #include "host.hpp"
 
 namespace moonep {
@@ -51,13 +52,6 @@ struct RouterArgs {
 
 __device__ __forceinline__ int expert_of(int i) {
   return ((i >> 1) << 7) + 2 * lane_id() + (i & 1);
-}
-
-// Two fp32 values as packed bf16, rounded to nearest even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // One logit, at any alignment.
