@@ -280,14 +280,14 @@ __global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router
   }
 }
 
-// Tokens per workgroup of a forward call that keeps sums in at most `most`
-// workgroups: whole rounds of its waves.
-inline int stats_chunk(int T, int most) {
+// Tokens per workgroup of a forward call of at most `most` workgroups: whole
+// rounds of its waves.
+inline int chunk_for(int T, int most) {
   const int rounds = (T + most * kRtWaves - 1) / (most * kRtWaves);
   return kRtWaves * (rounds > 1 ? rounds : 1);
 }
 inline int chunks_of(int T, int chunk) { return (T + chunk - 1) / chunk; }
-inline int max_chunks(int T) { return chunks_of(T, stats_chunk(T, kRtMaxChunks)); }
+inline int max_chunks(int T) { return chunks_of(T, chunk_for(T, kRtMaxChunks)); }
 
 // Rows times slices of experts up to which one workgroup joins a sequence.
 constexpr int kJoinOne = 512;
@@ -327,7 +327,7 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
   a.scale = r->scale;
   int chunks = 0;
   if (stats) {
-    a.chunk = stats_chunk(a.T, select ? kRtSelectChunks : kRtMaxChunks);
+    a.chunk = chunk_for(a.T, select ? kRtSelectChunks : kRtMaxChunks);
     chunks = chunks_of(a.T, a.chunk);
     const size_t rows = part_rows(a.T, a.nseq) * a.E, sums = sum_rows(a.T, a.nseq) * a.E;
     a.sum_p = reinterpret_cast<double*>(workspace);
@@ -335,7 +335,7 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
     a.part_c = reinterpret_cast<int32_t*>(a.part_p + rows);
     a.sum_c = a.part_c + rows;
   } else {
-    a.chunk = kRtWaves;
+    a.chunk = chunk_for(a.T, a.bias ? kRtSelectChunks : kRtMaxChunks);
   }
   if (a.T > 0) {
     const int grid = stats ? chunks : (a.T + a.chunk - 1) / a.chunk;
