@@ -90,7 +90,9 @@ __global__ __launch_bounds__(kQ8Threads) void k_q8_load(const q8_u32x2* __restri
 }
 
 // Dispatch from codes: one workgroup per token, its row decoded once and
-// written to each of its K places.
+// written to each of its K places.  Bound by the writes of scattered rows, as
+// the dispatch of bf16 rows is: 65,536 rows of 7,168 to 8 places in 1.50 ms,
+// 5.35 TB/s (non-temporal stores: 1.54 ms).
 template <int Q>
 __global__ __launch_bounds__(256) void k_dispatch_q8(const q8_u32x2* __restrict__ xq,
                                                      const uint8_t* __restrict__ xs,
@@ -126,6 +128,8 @@ __global__ __launch_bounds__(256) void k_dispatch_q8(const q8_u32x2* __restrict_
 // Backward of act = silu(gate) * up from the codes of h13, with s = 1 / (1 + e^-gate):
 //   d gate = d act * up * s * (1 + gate * (1 - s)),  d up = d act * gate * s,
 // and act = gate * s * up again for the second projection's weight gradient.
+// One workgroup per row; 65,536 rows of 2 x 2,048 in 0.209 ms, 6.5 TB/s (two
+// thirds of it writes).  From bf16 h13, without act: 0.236 ms.
 __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __restrict__ hq,
                                                               const uint8_t* __restrict__ hs,
                                                               const u32x4* dact, u32x4* dh13,
@@ -169,7 +173,9 @@ __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __
 //   dy[route_k] = g_k * dout[t],  dgates[t, k] = sum_h dout[t, h] * y[route_k, h].
 // Thread i takes vectors i + 256 u of the row.  The codes of KB routes are in
 // flight before the first is used; each wave sums its part of their KB dots,
-// and the four waves' parts are added in LDS, pass after pass.
+// and the four waves' parts are added in LDS, pass after pass.  Bound by the
+// scattered rows: 524,288 of 2,048 values in 0.70 ms, 5.0 TB/s (4 routes in
+// flight: 0.71, 2: 0.76; a wave per token: 0.70).
 template <int CU, int KB>
 __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict__ dout,
                                                         const q8_u32x2* __restrict__ yq,

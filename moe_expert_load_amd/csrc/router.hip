@@ -11,7 +11,9 @@ namespace moonep {
 // sequence and writes the results.  k_router_join<false>: a workgroup has one
 // slice and one of gridDim.z parts of the rows, and writes sums that
 // k_router_total adds up.  Its 16 waves are 16 / ns groups that take the rows in
-// turn, eight loads in flight each.
+// turn, eight loads in flight each.  One sequence of 65,536 tokens of 384
+// experts: 4.4 us and 2.5 for the total, against 123 in one workgroup and 8.7
+// without the parts.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinWaves = kJoinThreads / kWave;
 
@@ -142,6 +144,11 @@ __global__ __launch_bounds__(kTotalThreads) void k_router_total(RouterArgs a, in
 //   renormalised               scale w_k (dg_k - sum dg w) (1 - s_k for sigmoid),
 //   sigmoid, not renormalised  scale dg_k s_k (1 - s_k).
 // These K values reach the lanes that hold their experts through an LDS row.
+//
+// It streams: 65,536 fp32 tokens of 384 experts in 40 us (logits in, dlogits
+// out: 5.0 TB/s), 262,144 bf16 tokens of 896 in 181 us (5.2 TB/s; a device copy
+// reaches 4.8-4.9).  Five waves a SIMD for rows of 9 to 14 registers cost a few
+// spills and hide more: 181 us against 198 with four, 294 with six.
 // A gradient of renormalised gates alone reads only the K chosen logits.
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT>
@@ -289,7 +296,9 @@ inline int chunk_for(int T, int most) {
 inline int chunks_of(int T, int chunk) { return (T + chunk - 1) / chunk; }
 inline int max_chunks(int T) { return chunks_of(T, chunk_for(T, kRtMaxChunks)); }
 
-// Rows times slices of experts up to which one workgroup joins a sequence.
+// Rows times slices of experts up to which one workgroup joins a sequence: at
+// 512 rows of one slice it takes 4-5 us, as k_router_join<false> does alone,
+// and a launch of 2.5-4.8 us less follows.
 constexpr int kJoinOne = 512;
 
 // Parts into which a sequence's rows are joined first: several where a sequence

@@ -229,6 +229,8 @@ __device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, cons
 
 // The K largest keys in order, equal ones in ascending expert; lane k returns
 // the k-th id.  key is consumed.  Any keys: K rounds of a maximum of the wave.
+// For rows that sort_top leaves (NaN, masks, many equal keys): used for all rows
+// of 896 experts and K = 16 it takes 1,174 us where sort_top takes 202.
 template <int P>
 __device__ __forceinline__ int take_top(int (&key)[P], int K) {
   const int lane = lane_id();
@@ -353,7 +355,9 @@ __device__ __forceinline__ int count_before(const KeyList& list, int cnt, float 
 // Sorts the cnt <= 64 keys that m marks across the lanes, largest first, equal
 // ones in ascending expert: lane k < cnt gets the k-th key and its expert.
 // They are written to the list in ascending expert, each one's place in the
-// order is counted, and that is where its lane sends it.
+// order is counted, and that is where its lane sends it.  (Inserting one key
+// after the other into a list across the lanes, a median of three a key, took
+// 316 us where this takes 202: a chain of 20 steps with their scalar loop.)
 template <int P>
 __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_t (&m)[P],
                                             int cnt, KeyList& list, float& mykey, int& mine) {
@@ -605,6 +609,14 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // workgroup the counts in LDS; both go to row (workgroup + sequence) of the
 // workspace when the sequence or the chunk ends.  Along the tokens either
 // number grows, so no two pieces share a row.
+//
+// Bound by the vector units: 65,536 tokens of 384 experts (sigmoid, bias, K 8,
+// loss) take 45 us, 282 vector instructions a token, where reading the logits
+// takes 20; 262,144 bf16 tokens of 896 (softmax, K 16, loss) 202 us, 308 a token
+// in 80 % of the cycles, reading 97.  Without a choice (given ids) it streams:
+// 65,536 bf16 tokens of 384 in 11 us, 4.6 TB/s.  One wave a row, rather than 16
+// lanes and four rows a wave, keeps the K-independent work (scores, sums) at one
+// instruction per 64 experts and the row in P registers.
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
 __global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterArgs a) {
