@@ -511,7 +511,8 @@ int moe_balance_loss(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void 
  *              + dloss[q] d loss[q] / d z
  * The choice of experts and the counts are constants.  Written whole, rounded
  * once, in the logits' type; a token of no sequence has no second part.  An id
- * outside [0, E) contributes nothing.  dlogits may be logits (in place).
+ * outside [0, E) contributes nothing.  dlogits may be logits (in place) and
+ * must not overlap it otherwise.
  * topk_ids is read only with dgates, counts and cu_tokens only with dloss; at
  * least one of dgates and dloss is given.
  */
@@ -532,7 +533,8 @@ int moe_router_backward(const moe_cfg *cfg, const moe_router_cfg *rcfg, const vo
  * A value that is not finite becomes NaN and takes no part in the scale.
  *   q     [rows][width] uint8, the codes (base on a 16-byte boundary)
  *   scale [rows][ceil(width/32)] uint8, k + 127
- * What a code stands for, code * 2^k, is exact in bf16.
+ * What a code stands for, code * 2^k, is exact in bf16.  The three tensors
+ * must not overlap.
  * width % 8 == 0, width >= 8, rows >= 0; rows * ceil(width/32) * 32 < 2^37
  * (MOE_ELIMIT).
  */

@@ -4,6 +4,7 @@
 // of y.  The format is in q8.hpp.  All of them stream: what they cost is the
 // bytes of their tensors.
 #include "convert.hpp"
+#include "overlap.hpp"
 #include "host.hpp"
 #include "q8.hpp"
 
@@ -259,10 +260,12 @@ inline int check_q8(int64_t rows, int32_t width, int64_t* tiles) {
   return *tiles >= (int64_t(1) << 24) ? MOE_ELIMIT : MOE_OK;
 }
 
-// Whether two byte ranges share memory.
-inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+// Whether bf16 rows share memory with their codes or scales, or those with each
+// other: a workgroup would write what another has yet to read.
+inline bool q8_overlap(int64_t rows, int hv, int hvp, const void* x, const void* q,
+                       const void* scale) {
+  const int64_t n = rows * hv * 8, ns = rows * (hvp / 4);
+  return overlap(x, 2 * n, q, n) || overlap(x, 2 * n, scale, ns) || overlap(q, n, scale, ns);
 }
 
 }  // namespace moonep
@@ -277,6 +280,7 @@ extern "C" int moe_q8_store(int64_t rows, int32_t width, const moe_bf16* src, ui
   if (rows == 0) return MOE_OK;
   if (!src || !q || !scale || !aligned16(src, q)) return MOE_EINVAL;
   const int hv = width / 8, hvp = (hv + 3) / 4 * 4;
+  if (q8_overlap(rows, hv, hvp, src, q, scale)) return MOE_EINVAL;
   const u32x4* s = reinterpret_cast<const u32x4*>(src);
   q8_u32x2* d = reinterpret_cast<q8_u32x2*>(q);
   const dim3 grid((unsigned)tiles), block(kQ8Threads);
@@ -295,6 +299,7 @@ extern "C" int moe_q8_load(int64_t rows, int32_t width, const uint8_t* q, const 
   if (rows == 0) return MOE_OK;
   if (!dst || !q || !scale || !aligned16(dst, q)) return MOE_EINVAL;
   const int hv = width / 8, hvp = (hv + 3) / 4 * 4;
+  if (q8_overlap(rows, hv, hvp, dst, q, scale)) return MOE_EINVAL;
   const q8_u32x2* s = reinterpret_cast<const q8_u32x2*>(q);
   u32x4* d = reinterpret_cast<u32x4*>(dst);
   const dim3 grid((unsigned)tiles), block(kQ8Threads);

@@ -2,6 +2,7 @@
 // points.  The formulas, the row layout and the forward are in router.hpp.
 #include <algorithm>
 
+#include "overlap.hpp"
 #include "router.hpp"
 
 namespace moonep {
@@ -440,6 +441,8 @@ extern "C" int moe_router_backward(const moe_cfg* cfg, const moe_router_cfg* rcf
   if (!logits || !dlogits || (dgates && !topk_ids)) return MOE_EINVAL;
   if (!aligned16(logits, static_cast<const void*>(dlogits)) || !aligned16(dgates, dloss))
     return MOE_EINVAL;
+  const int64_t bytes = int64_t(cfg->R) * cfg->S * cfg->E * (rcfg->logits_bf16 ? 2 : 4);
+  if (dlogits != logits && overlap(logits, bytes, dlogits, bytes)) return MOE_EINVAL;
   RouterArgs a{};
   a.logits = logits;
   a.ids = const_cast<int32_t*>(topk_ids);

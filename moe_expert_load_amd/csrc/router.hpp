@@ -177,10 +177,11 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 constexpr float kDeep = -60.f;
 
 // Sums of exponentials in this range are taken as they are: the largest logit
-// is then between -15 and 13, so nothing overflows or underflows, and the
-// exponentials' errors are those of arguments of at most 15.  Other sums
-// (far logits, a masked row's 0, NaN) are taken again from z - max.
-constexpr float kPlainLo = 0x1p-10f, kPlainHi = 0x1p18f;
+// is then between -8 and 13, so nothing overflows, a share that underflows is
+// below 2^-126 itself, and the exponentials' arguments are longer than those of
+// z - max by 13 at most.  Other sums (far logits, a masked row's 0, NaN) are
+// taken again from z - max.
+constexpr float kPlainLo = 1.f, kPlainHi = 0x1p18f;
 // The same for sums of sigmoids: none of their terms that count has underflowed.
 constexpr float kSigmoidLo = 0x1p-60f;
 

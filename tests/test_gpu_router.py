@@ -482,6 +482,52 @@ def test_rows_of_one_wave_in_any_order():
         assert np.all(np.abs(sg - sk[:, :-1]) <= 16 * 2.0 ** -52 * sk[:, :-1])
 
 
+@pytest.mark.parametrize("E,K,bf16", [(2048, 8, False), (60, 3, True)])
+def test_captured_calls_equal_eager(E, K, bf16):
+    """Forward with the loss and backward captured once, replayed on new logits and sequences;
+    2,048 experts take more LDS than a launch gets unasked."""
+    R, S, nseq = 2, 150, 4
+    T = R * S
+    c = cfg_of(R, S, E, K)
+    rc = mx.make_router_cfg(O.SIGMOID, 1, 1.5, bf16, nseq)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    z, bias = torch.zeros((T, E), dtype=dt, device="cuda"), torch.zeros(E, device="cuda")
+    cu = torch.zeros(nseq + 1, dtype=torch.int32, device="cuda")
+    ids, gates = torch.zeros((T, K), dtype=torch.int32, device="cuda"), torch.zeros((T, K), device="cuda")
+    counts, prob = torch.zeros((nseq, E), dtype=torch.int32, device="cuda"), torch.zeros((nseq, E), device="cuda")
+    loss, dl, dg = torch.zeros(nseq, device="cuda"), torch.ones(nseq, device="cuda"), torch.ones((T, K), device="cuda")
+    ws = torch.zeros(mx.moe_router_workspace_size(c, rc), dtype=torch.uint8, device="cuda")
+    dz = torch.zeros_like(z)
+
+    def step():
+        mx.moe_router(c, rc, z, bias, ids, gates, cu, counts, prob, loss, ws)
+        mx.moe_router_backward(c, rc, z, ids, dg, cu, counts, dl, dz)
+
+    def out():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (ids, gates, counts, prob, loss, dz.view(torch.int16) if bf16 else dz)]
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2, 3):
+        r = np.random.default_rng(seed)
+        z.copy_(torch.from_numpy(r.standard_normal((T, E))))
+        bias.copy_(torch.from_numpy(0.1 * r.standard_normal(E)))
+        dg.copy_(torch.from_numpy(r.standard_normal((T, K))))
+        cu.copy_(torch.from_numpy(cuts(T, nseq, seed, tail=5)))
+        torch.cuda.synchronize()
+        g.replay()
+        a = out()
+        step()
+        b = out()
+        g.replay()
+        for x, y, w in zip(a, b, out()):
+            assert torch.equal(x, y) and torch.equal(y, w)
+
+
 def test_one_device(monkeypatch):
     c = cfg_of(1, 4, 8, 2)
     rc = mx.make_router_cfg(O.SOFTMAX, 1)

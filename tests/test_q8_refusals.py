@@ -36,11 +36,15 @@ def test_rows_and_widths(lib, name):
         args[i] = None
         assert f(4, 64, *args, None) == E
     # bf16 rows and codes on 16-byte boundaries; scale bytes anywhere
-    assert f(4, 64, M, A, A, None) == E
-    if name == "moe_q8_store":
-        assert f(4, 64, A, M, A, None) == E
-    else:
-        assert f(4, 64, A, A, M, None) == E
+    order = (lambda x, q, s: (x, q, s)) if name == "moe_q8_store" else (lambda x, q, s: (q, s, x))
+    B, C = at(1 << 16), at(1 << 17)
+    assert f(4, 64, *order(M, B, C), None) == E
+    assert f(4, 64, *order(A, at((1 << 16) + 8), C), None) == E
+    # 512 bytes of rows, 256 of codes, 8 of scales: no two may share memory
+    assert f(4, 64, *order(A, at(496), C), None) == E
+    assert f(4, 64, *order(at(240), A, C), None) == E
+    assert f(4, 64, *order(A, B, at(511)), None) == E
+    assert f(4, 64, *order(A, B, at((1 << 16) + 255)), None) == E
 
 
 def test_dispatch_and_combine(lib):

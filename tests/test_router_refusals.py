@@ -86,6 +86,10 @@ def test_missing_and_misaligned(lib):
     assert lib.moe_balance_loss(c, r, M, A, None, A, A, A, A, None) == E
     assert lib.moe_router_backward(c, r, A, A, A, None, A, A, M, None) == E
     assert lib.moe_router_backward(c, r, A, A, M, None, A, A, A, None) == E
+    # dlogits over a part of logits (4 x 8 fp32 = 128 bytes)
+    for off in (16, 112, -112):
+        part = ctypes.c_void_p((1 << 20) + off)
+        assert lib.moe_router_backward(c, r, A, A, A, None, A, A, part, None) == E
 
 
 def test_workspace_size_covers_every_piece():
