@@ -620,19 +620,24 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // instruction per 64 experts and the row in P registers.
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
-__global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterArgs a) {
-  extern __shared__ float lds[];                  // [waves][E] sums, [E] counts
+__global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterArgs a) {
+  // STATS: [waves][E] sums, [E] counts; BIAS: [64 P] bias, -inf past E (in LDS
+  // for all waves: in registers it cost the rows of 896 experts spills)
+  extern __shared__ __attribute__((aligned(16))) float lds[];
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
   __shared__ __attribute__((aligned(16))) KeyList lists[SELECT ? kRtWaves : 1];
   KeyList& list = lists[SELECT ? wv : 0];
   int probe = kKeyNone;
-  int* cnt = reinterpret_cast<int*>(lds + kRtWaves * E);
+  float* sum = lds + (BIAS ? 64 * P : 0);
+  int* cnt = reinterpret_cast<int*>(sum + kRtWaves * E);
   const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-  float acc[P], bias[P];
+  float acc[P];
+  Row<P, BF16> next;
+  if (t0 + wv < t1) load_row<P, BF16, FULL>(a.logits, t0 + wv, E, next);
   if constexpr (BIAS) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) bias[i] = FULL || expert_of(i) < E ? a.bias[expert_of(i)] : -INFINITY;
+    for (int e = threadIdx.x; e < 64 * P; e += kRtThreads) lds[e] = e < E ? a.bias[e] : -INFINITY;
+    if constexpr (!STATS) __syncthreads();
   }
   for (int lo = t0; lo < t1;) {
     int hi = t1, seq = -1;
@@ -645,8 +650,7 @@ __global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterAr
       __syncthreads();
     }
     if (SELECT || seq >= 0) {
-      Row<P, BF16> next;
-      if (lo + wv < hi) load_row<P, BF16, FULL>(a.logits, lo + wv, E, next);
+      if (lo != t0 && lo + wv < hi) load_row<P, BF16, FULL>(a.logits, lo + wv, E, next);
       for (int t = lo + wv; t < hi; t += kRtWaves) {
         float z[P], v[P], co[P];
         unpack_row<P, BF16>(next, z);
@@ -675,9 +679,11 @@ __global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterAr
             }
             float least = z[0];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-              least = fminf(least, z[i]);
-              v[i] = SOFT ? fmaf(v[i], inv, bias[i]) : v[i] + bias[i];
+            for (int i = 0; i < P; i += 2) {
+              const float2 b = *reinterpret_cast<const float2*>(lds + expert_of(i));
+              least = fminf(least, fminf(z[i], z[i + 1]));
+              v[i] = SOFT ? fmaf(v[i], inv, b.x) : v[i] + b.x;
+              v[i + 1] = SOFT ? fmaf(v[i + 1], inv, b.y) : v[i + 1] + b.y;
             }
             if (ballot(least == -INFINITY)) {             // masked, whatever their bias
 #pragma unroll
@@ -705,7 +711,7 @@ __global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterAr
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int e = expert_of(i);
-          if (FULL || e < E) lds[wv * E + e] = acc[i];
+          if (FULL || e < E) sum[wv * E + e] = acc[i];
         }
       }
       __syncthreads();
@@ -714,7 +720,7 @@ __global__ __launch_bounds__(kRtThreads, P <= 14 ? 4 : 2) void k_router(RouterAr
         for (int e = threadIdx.x; e < E; e += kRtThreads) {
           float s = 0.f;
 #pragma unroll
-          for (int w = 0; w < kRtWaves; ++w) s += lds[w * E + e];
+          for (int w = 0; w < kRtWaves; ++w) s += sum[w * E + e];
           a.part_p[row + e] = s;
           a.part_c[row + e] = cnt[e];
         }
@@ -743,7 +749,9 @@ inline int with_row(int E, bool bf16, F f) {
   MOE_ROW(4)
   MOE_ROW(6)
   MOE_ROW(8)
+  MOE_ROW(12)
   MOE_ROW(14)
+  MOE_ROW(16)
   MOE_ROW(20)
   MOE_ROW(32)
 #undef MOE_ROW
@@ -755,11 +763,12 @@ inline int with_row(int E, bool bf16, F f) {
 template <bool SOFT>
 int launch_forward(const RouterArgs& a, bool bf16, bool select, bool stats, int grid,
                    hipStream_t stream) {
-  const size_t lds = stats ? size_t(kRtWaves + 1) * a.E * 4 : 0;
+  const size_t stats_lds = stats ? size_t(kRtWaves + 1) * a.E * 4 : 0;
   return with_row(a.E, bf16, [&](auto p, auto b, auto full) {
     constexpr int P = decltype(p)::value;
     constexpr bool BF = decltype(b)::value, FULL = decltype(full)::value;
     const dim3 g(grid), t(kRtThreads);
+    const size_t lds = stats_lds + (select && a.bias ? size_t(64) * P * 4 : 0);
     int rc = MOE_OK;
 #define MOE_ROUTER(SEL, BIAS, STATS)                                         \
   do {                                                                       \

@@ -169,6 +169,9 @@ SHAPES = [  # R, S, E, K, nseq
     (1, 1, 1, 1, 1), (1, 1, 8, 8, 3), (2, 3, 8, 3, 2), (1, 33, 7, 2, 5), (1, 5, 65, 64, 2),
     (3, 11, 129, 5, 9), (8, 9, 384, 8, 4), (4, 13, 520, 12, 70), (1, 9, 897, 16, 1),
     (2, 8, 1280, 3, 2), (1, 6, 2048, 64, 2), (1, 5, 2047, 40, 3), (8, 520, 64, 4, 37),
+    # rows that fill the lanes, of every register count, and rows that nearly do
+    (1, 19, 128, 6, 3), (1, 9, 256, 4, 2), (2, 5, 512, 4, 1), (1, 9, 768, 5, 2), (1, 5, 896, 16, 3),
+    (1, 7, 1024, 8, 2), (1, 4, 1023, 9, 2), (1, 6, 702, 33, 2), (1, 3, 1536, 2, 1),
 ]
 
 
