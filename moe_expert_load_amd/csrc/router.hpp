@@ -231,7 +231,7 @@ __device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, cons
 // The K largest keys in order, equal ones in ascending expert; lane k returns
 // the k-th id.  key is consumed.  Any keys: K rounds of a maximum of the wave.
 // For rows that sort_top leaves (NaN, masks, many equal keys): used for all rows
-// of 896 experts and K = 16 it takes 1,174 us where sort_top takes 202.
+// of 896 experts and K = 16 it takes 1,174 us where sort_top takes 205.
 template <int P>
 __device__ __forceinline__ int take_top(int (&key)[P], int K) {
   const int lane = lane_id();
@@ -358,7 +358,7 @@ __device__ __forceinline__ int count_before(const KeyList& list, int cnt, float 
 // They are written to the list in ascending expert, each one's place in the
 // order is counted, and that is where its lane sends it.  (Inserting one key
 // after the other into a list across the lanes, a median of three a key, took
-// 316 us where this takes 202: a chain of 20 steps with their scalar loop.)
+// 316 us where this takes 205: a chain of 20 steps with their scalar loop.)
 template <int P>
 __device__ __forceinline__ void sort_marked(const float (&key)[P], const uint64_t (&m)[P],
                                             int cnt, KeyList& list, float& mykey, int& mine) {
@@ -612,8 +612,8 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // number grows, so no two pieces share a row.
 //
 // Bound by the vector units: 65,536 tokens of 384 experts (sigmoid, bias, K 8,
-// loss) take 45 us, 282 vector instructions a token, where reading the logits
-// takes 20; 262,144 bf16 tokens of 896 (softmax, K 16, loss) 202 us, 308 a token
+// loss) take 46 us, 282 vector instructions a token, where reading the logits
+// takes 20; 262,144 bf16 tokens of 896 (softmax, K 16, loss) 205 us, 308 a token
 // in 80 % of the cycles, reading 97.  Without a choice (given ids) it streams:
 // 65,536 bf16 tokens of 384 in 11 us, 4.6 TB/s.  One wave a row, rather than 16
 // lanes and four rows a wave, keeps the K-independent work (scores, sums) at one
@@ -621,8 +621,8 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // ---------------------------------------------------------------------------
 template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
 __global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterArgs a) {
-  // STATS: [waves][E] sums, [E] counts; BIAS: [64 P] bias, -inf past E (in LDS
-  // for all waves: in registers it cost the rows of 896 experts spills)
+  // BIAS: [64 P] bias, -inf past E (in registers it cost rows of 896 experts
+  // spills: 81 us for 32,768 tokens, 51 so); STATS: [waves][E] sums, [E] counts
   extern __shared__ __attribute__((aligned(16))) float lds[];
   const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int E = a.E, K = a.K;
@@ -732,7 +732,8 @@ __global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterAr
 }
 
 // Calls f with the registers per lane of a row of E experts, the type, and
-// whether the row fills all lanes.
+// whether the row fills all lanes.  The counts are close where experts are
+// many: 32,768 rows of 1,024 experts take 38 us in 16 registers, 98 in 20.
 template <typename F>
 inline int with_row(int E, bool bf16, F f) {
   const int p = 2 * ((E + 127) / 128);
