@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router
     float shift = 0.f, inv = 1.f;
     if (rows) {
       float z[P];
-      unpack_row<P, BF16>(next, z);
+      unpack_row<P, BF16, FULL>(next, E, z);
       if (t + 1 < t1) load_row<P, BF16, FULL>(a.logits, t + 1, E, next);
       inv = row_shares<P, BF16, FULL, SOFT, !SOFT>(a, t, z, v, co, shift);
     }
@@ -263,8 +263,9 @@ __global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router
 #pragma unroll
     for (int i = 0; i < P; i += 2) {
       const int e = expert_of(i);
+      const bool sure = FULL || i < kSure<P>;
       if (FULL || (E & 1) == 0) {
-        if (FULL || e < E) {
+        if (sure || e < E) {
           if constexpr (BF16)
             *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.dlogits) + at + e) =
                 cvt_bf16x2(dz[i], dz[i + 1]);
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(kRtThreads, P > 8 && P <= 14 ? 5 : 1) void k_router
         const uint32_t w = BF16 ? cvt_bf16x2(dz[i], dz[i + 1]) : 0u;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (e + j < E) {
+          if (sure || e + j < E) {
             if constexpr (BF16)
               reinterpret_cast<uint16_t*>(a.dlogits)[at + e + j] = (uint16_t)(w >> (16 * j));
             else

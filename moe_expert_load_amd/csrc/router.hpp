@@ -68,47 +68,50 @@ struct Row {
   uint32_t w[BF16 ? P / 2 : P];
 };
 
+// The registers of a row that hold experts in every lane: a row of P has more
+// than 64 kSure<P> experts (with_row).
+template <int P>
+constexpr int kSure = P <= 8 ? P - 2 : P == 12 ? 8 : P <= 16 ? P - 2 : P == 20 ? 16 : 20;
+
+// Lanes past E load experts before it, which unpack_row replaces: a load under a
+// condition costs more (32,768 fp32 rows of 704 experts: routes 24 us, 21 so).
 template <int P, bool BF16, bool FULL>
 __device__ __forceinline__ void load_row(const void* z, int64_t t, int E, Row<P, BF16>& r) {
-  constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;     // -inf past E
-  const int64_t at = t * E;
+  using T = std::conditional_t<BF16, uint16_t, uint32_t>;
+  using Pair = std::conditional_t<BF16, uint32_t, uint2>;
+  const T* p = reinterpret_cast<const T*>(z) + t * E;
 #pragma unroll
   for (int i = 0; i < P; i += 2) {
     const int e = expert_of(i);
-    if constexpr (BF16) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(z) + at;
-      if (FULL || (E & 1) == 0) {
-        r.w[i / 2] = kNone;
-        if (FULL || e < E) r.w[i / 2] = *reinterpret_cast<const uint32_t*>(p + e);
+    const bool sure = FULL || i < kSure<P>;
+    if (FULL || (E & 1) == 0) {
+      const Pair v = *reinterpret_cast<const Pair*>(p + (sure ? e : min(e, E - 2)));
+      if constexpr (BF16) {
+        r.w[i / 2] = v;
       } else {
-        uint32_t lo = 0xff80u, hi = 0xff80u;
-        if (e < E) lo = p[e];
-        if (e + 1 < E) hi = p[e + 1];
-        r.w[i / 2] = lo | (hi << 16);
+        r.w[i] = v.x;
+        r.w[i + 1] = v.y;
       }
     } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(z) + at;
-      if (FULL || (E & 1) == 0) {
-        r.w[i] = r.w[i + 1] = kNone;
-        if (FULL || e < E) {
-          const uint2 v = *reinterpret_cast<const uint2*>(p + e);
-          r.w[i] = v.x;
-          r.w[i + 1] = v.y;
-        }
+      const uint32_t lo = p[sure ? e : min(e, E - 1)], hi = p[sure ? e + 1 : min(e + 1, E - 1)];
+      if constexpr (BF16) {
+        r.w[i / 2] = lo | (hi << 16);
       } else {
-        r.w[i] = e < E ? p[e] : kNone;
-        r.w[i + 1] = e + 1 < E ? p[e + 1] : kNone;
+        r.w[i] = lo;
+        r.w[i + 1] = hi;
       }
     }
   }
 }
 
-template <int P, bool BF16>
-__device__ __forceinline__ void unpack_row(const Row<P, BF16>& r, float (&v)[P]) {
+// The row's logits, -inf past E.
+template <int P, bool BF16, bool FULL>
+__device__ __forceinline__ void unpack_row(const Row<P, BF16>& r, int E, float (&v)[P]) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     if constexpr (BF16) v[i] = (i & 1) ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
     else v[i] = __uint_as_float(r.w[i]);
+    if (!FULL && i >= kSure<P>) v[i] = expert_of(i) < E ? v[i] : -INFINITY;
   }
 }
 
@@ -214,7 +217,7 @@ __device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, cons
   Row<P, BF16> again;
   load_row<P, BF16, FULL>(a.logits, t, a.E, again);
   float x[P];
-  unpack_row<P, BF16>(again, x);
+  unpack_row<P, BF16, FULL>(again, a.E, x);
   const float m = wave_max_f(lane_max<P>(x));
   if (!SOFT && !(m < kDeep)) return recip(sum);              // NaN, for one
   sum = 0.f;
@@ -554,7 +557,7 @@ __device__ __forceinline__ int choose(const RouterArgs& a, int64_t t, const floa
   int key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    key[i] = FULL || expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
+    key[i] = FULL || i < kSure<P> || expert_of(i) < a.E ? order_key(z[i]) : kKeyNone;
   id = take_top<P>(key, a.K);
   zk = logit_at<BF16>(a.logits, t * a.E + (lane_id() < a.K ? id : 0));
   return id;
@@ -619,8 +622,14 @@ __device__ __forceinline__ int sequence_of(const RouterArgs& a, int t, int& end)
 // lanes and four rows a wave, keeps the K-independent work (scores, sums) at one
 // instruction per 64 experts and the row in P registers.
 // ---------------------------------------------------------------------------
+// Waves a SIMD.  Two leave 256 registers: 32,768 sigmoid rows of 1,024 experts
+// with bias take 62-65 us with two, 65-76 with four and their spills; of a
+// softmax 61-66 and 47-57.
+template <int P, bool SOFT, bool BIAS>
+constexpr int kForwardWaves = P < 16 || (P == 16 && (SOFT || !BIAS)) ? 4 : 2;
+
 template <int P, bool BF16, bool FULL, bool SOFT, bool SELECT, bool BIAS, bool STATS>
-__global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterArgs a) {
+__global__ __launch_bounds__(kRtThreads, (kForwardWaves<P, SOFT, BIAS>)) void k_router(RouterArgs a) {
   // BIAS: [64 P] bias, -inf past E (in registers it cost rows of 896 experts
   // spills: 81 us for 32,768 tokens, 51 so); STATS: [waves][E] sums, [E] counts
   extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -653,7 +662,7 @@ __global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterAr
       if (lo != t0 && lo + wv < hi) load_row<P, BF16, FULL>(a.logits, lo + wv, E, next);
       for (int t = lo + wv; t < hi; t += kRtWaves) {
         float z[P], v[P], co[P];
-        unpack_row<P, BF16>(next, z);
+        unpack_row<P, BF16, FULL>(next, E, z);
         if (t + kRtWaves < hi) load_row<P, BF16, FULL>(a.logits, t + kRtWaves, E, next);
         int id = -1;
         if constexpr (!SELECT) {
@@ -711,7 +720,7 @@ __global__ __launch_bounds__(kRtThreads, P <= 16 ? 4 : 2) void k_router(RouterAr
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int e = expert_of(i);
-          if (FULL || e < E) sum[wv * E + e] = acc[i];
+          if (FULL || i < kSure<P> || e < E) sum[wv * E + e] = acc[i];
         }
       }
       __syncthreads();

@@ -172,6 +172,10 @@ SHAPES = [  # R, S, E, K, nseq
     # rows that fill the lanes, of every register count, and rows that nearly do
     (1, 19, 128, 6, 3), (1, 9, 256, 4, 2), (2, 5, 512, 4, 1), (1, 9, 768, 5, 2), (1, 5, 896, 16, 3),
     (1, 7, 1024, 8, 2), (1, 4, 1023, 9, 2), (1, 6, 702, 33, 2), (1, 3, 1536, 2, 1),
+    # the least experts of every register count, even and odd
+    (1, 3, 2, 2, 1), (1, 9, 130, 4, 2), (1, 9, 258, 4, 2), (1, 7, 386, 6, 2), (1, 7, 514, 6, 2),
+    (1, 5, 770, 7, 2), (1, 5, 898, 7, 2), (1, 5, 1026, 7, 2), (1, 5, 1282, 7, 2),
+    (1, 5, 257, 4, 2), (1, 5, 513, 6, 2), (1, 3, 769, 5, 2), (1, 3, 1025, 5, 2), (1, 3, 1281, 5, 2),
 ]
 
 
