@@ -302,6 +302,11 @@ inline int max_chunks(int T) { return chunks_of(T, chunk_for(T, kRtMaxChunks)); 
 // 512 rows of one slice it takes 4-5 us, as k_router_join<false> does alone,
 // and a launch of 2.5-4.8 us less follows.
 constexpr int kJoinOne = 512;
+// Sequences from which on one workgroup joins each, whatever its rows: with
+// workgroups for its slices too, most have a row or two.  The loss of 65,536
+// bf16 tokens of 896 experts takes 35 us for 512 sequences and 271 for 16,384
+// (63 and 1,118 with slices); 89 against 66 if one of the 512 has half of them.
+constexpr int kJoinMany = 512;
 
 // Parts into which a sequence's rows are joined first: several where a sequence
 // has 256 rows or more on average (fewer leave a wave one round of loads).
@@ -358,7 +363,7 @@ inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, 
   if (stats) {
     const int slices = (a.E + kWave - 1) / kWave;
     const dim3 t(kJoinThreads);
-    if (slices <= kJoinWaves && chunks * slices <= kJoinOne) {
+    if (slices <= kJoinWaves && (chunks * slices <= kJoinOne || a.nseq >= kJoinMany)) {
       hipLaunchKernelGGL(k_router_join<true>, dim3(a.nseq), t, 0, stream, a, chunks, slices,
                          counts, prob, loss);
       return hip_status();

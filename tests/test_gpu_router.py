@@ -172,6 +172,8 @@ SHAPES = [  # R, S, E, K, nseq
     # rows that fill the lanes, of every register count, and rows that nearly do
     (1, 19, 128, 6, 3), (1, 9, 256, 4, 2), (2, 5, 512, 4, 1), (1, 9, 768, 5, 2), (1, 5, 896, 16, 3),
     (1, 7, 1024, 8, 2), (1, 4, 1023, 9, 2), (1, 6, 702, 33, 2), (1, 3, 1536, 2, 1),
+    # more sequences than 512, most of them of a token or none
+    (1, 700, 130, 4, 600), (1, 90, 1100, 3, 520),
     # the least experts of every register count, even and odd
     (1, 3, 2, 2, 1), (1, 9, 130, 4, 2), (1, 9, 258, 4, 2), (1, 7, 386, 6, 2), (1, 7, 514, 6, 2),
     (1, 5, 770, 7, 2), (1, 5, 898, 7, 2), (1, 5, 1026, 7, 2), (1, 5, 1282, 7, 2),
