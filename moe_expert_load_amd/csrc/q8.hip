@@ -3,6 +3,8 @@
 // backward of the SwiGLU activation and of combine from the codes of h13 and
 // of y.  The format is in q8.hpp.  All of them stream: what they cost is the
 // bytes of their tensors.
+#include <algorithm>
+
 #include "convert.hpp"
 #include "overlap.hpp"
 #include "host.hpp"
@@ -130,17 +132,22 @@ __global__ __launch_bounds__(256) void k_dispatch_q8(const q8_u32x2* __restrict_
 //   d gate = d act * up * s * (1 + gate * (1 - s)),  d up = d act * gate * s,
 // and act = gate * s * up again for the second projection's weight gradient.
 // One workgroup per row; 65,536 rows of 2 x 2,048 in 0.209 ms, 6.5 TB/s (two
-// thirds of it writes).  From bf16 h13, without act: 0.236 ms.
+// thirds of it writes).  From bf16 h13, without act: 0.236 ms.  Rows below 64
+// vectors share a workgroup: 262,144 of 2 x 256 values take 121 us, 196 with one
+// each; wider ones do not gain (2 x 512: 231 and 226, 2 x 1,024: 460 and 431).
 __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __restrict__ hq,
                                                               const uint8_t* __restrict__ hs,
                                                               const u32x4* dact, u32x4* dh13,
                                                               u32x4* act,       // may be dact
-                                                              int64_t rows, int hv) {
+                                                              int64_t rows, int hv, int per) {
   const int sb = (hv + 3) >> 2;                    // scale bytes of one half row
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  const int sub = per > 1 ? (int)threadIdx.x / hv : 0;
+  const int first = (int)threadIdx.x - sub * hv;
+  if (sub >= per) return;
+  for (int64_t r = int64_t(blockIdx.x) * per + sub; r < rows; r += int64_t(gridDim.x) * per) {
     const q8_u32x2* gq = hq + r * 2 * hv;
     const uint8_t* gs = hs + r * 2 * sb;
-    for (int c = threadIdx.x; c < hv; c += kQ8Threads) {
+    for (int c = first; c < hv; c += kQ8Threads) {
       const u32x4 dw = dact[r * hv + c];
       float g[8], x[8];
       q8_decode(gq[c], gs[c >> 2], g);
@@ -170,33 +177,40 @@ __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __
   }
 }
 
-// Backward of combine from the codes of y: one workgroup per token,
+// Backward of combine from the codes of y: W = 4 waves, or 1, per token,
 //   dy[route_k] = g_k * dout[t],  dgates[t, k] = sum_h dout[t, h] * y[route_k, h].
-// Thread i takes vectors i + 256 u of the row.  The codes of KB routes are in
+// Thread i takes vectors i + 64 W u of the row.  The codes of KB routes are in
 // flight before the first is used; each wave sums its part of their KB dots,
 // and the four waves' parts are added in LDS, pass after pass.  Bound by the
 // scattered rows: 524,288 of 2,048 values in 0.70 ms, 5.0 TB/s (4 routes in
-// flight: 0.71, 2: 0.76; a wave per token: 0.70).
-template <int CU, int KB>
+// flight: 0.71, 2: 0.76).  One wave takes rows of up to 128 vectors, whose
+// workgroups have too few loads in flight: 262,144 of 512 values in 81 us, 1,024
+// in 189, against 220 and 232 with four waves; of 2,048 both take 0.70 ms.
+template <int W, int CU, int KB>
 __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict__ dout,
                                                         const q8_u32x2* __restrict__ yq,
                                                         const uint8_t* __restrict__ ys,
                                                         const float* __restrict__ gates,
                                                         const int32_t* __restrict__ route,
                                                         u32x4* __restrict__ dy,
-                                                        float* __restrict__ dgates, int K,
-                                                        int hv) {
-  __shared__ float s_dot[4][MOE_MAX_K];
-  const int t = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wv = tid / kWave;
+                                                        float* __restrict__ dgates, int ntok,
+                                                        int K, int hv) {
+  constexpr int NT = W * kWave;                         // threads of a token
+  static_assert(W == 1 || W == 4);
+  __shared__ float s_dot[W][MOE_MAX_K];
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int t = W == 1 ? (int)blockIdx.x * 4 + wv : (int)blockIdx.x;
+  const int tid = W == 1 ? lane : (int)threadIdx.x;     // within the token
+  if (W == 1 && t >= ntok) return;
   const int sb = (hv + 3) >> 2;
   const int myroute = lane < K ? route[int64_t(t) * K + lane] : -1;
   const float mygate = lane < K ? gates[int64_t(t) * K + lane] : 0.f;
   float mydot = 0.f;                                    // lane k: this wave's part of k's dot
-  for (int c0 = 0; c0 < hv; c0 += 256 * CU) {
+  for (int c0 = 0; c0 < hv; c0 += NT * CU) {
     u32x4 d[CU];
 #pragma unroll
     for (int u = 0; u < CU; ++u) {
-      const int c = c0 + u * 256 + tid;
+      const int c = c0 + u * NT + tid;
       d[u] = c < hv ? __builtin_nontemporal_load(dout + int64_t(t) * hv + c) : u32x4{0, 0, 0, 0};
     }
     for (int k0 = 0; k0 < K; k0 += KB) {
@@ -209,7 +223,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
         const int64_t r = ok ? src : 0;
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-          const int c = c0 + u * 256 + tid;
+          const int c = c0 + u * NT + tid;
           v[kb][u] = q8_u32x2{0, 0};
           b[kb][u] = 127;
           if (ok && c < hv) {
@@ -226,7 +240,7 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
         float part = 0.f;
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-          const int c = c0 + u * 256 + tid;
+          const int c = c0 + u * NT + tid;
           float y[8];
           q8_decode(v[kb][u], b[kb][u], y);
           u32x4 o;
@@ -244,10 +258,14 @@ __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict_
       }
     }
   }
-  if (lane < K) s_dot[wv][lane] = mydot;
-  __syncthreads();
-  if (tid < K)
-    dgates[int64_t(t) * K + tid] = s_dot[0][tid] + s_dot[1][tid] + s_dot[2][tid] + s_dot[3][tid];
+  if constexpr (W == 1) {
+    if (lane < K) dgates[int64_t(t) * K + lane] = mydot;
+  } else {
+    if (lane < K) s_dot[wv][lane] = mydot;
+    __syncthreads();
+    if (tid < K)
+      dgates[int64_t(t) * K + tid] = s_dot[0][tid] + s_dot[1][tid] + s_dot[2][tid] + s_dot[3][tid];
+  }
 }
 
 // rows x width of moe_q8_store and moe_q8_load, and their grid of tiles.
@@ -348,11 +366,13 @@ extern "C" int moe_swiglu_backward_q8(const moe_cfg* cfg, const uint8_t* h13q,
       overlap(act, 2 * n, h13q, 2 * n) || overlap(act, 2 * n, h13scale, ns) ||
       (act != dact && overlap(act, 2 * n, dact, 2 * n)))
     return MOE_EINVAL;
-  const int64_t grid = rows < (int64_t(1) << 20) ? rows : (int64_t(1) << 20);
+  const int hv = cfg->Hp / 8;
+  const int per = hv < kWave ? kQ8Threads / hv : 1;               // rows of a workgroup
+  const int64_t grid = std::min<int64_t>((rows + per - 1) / per, int64_t(1) << 20);
   hipLaunchKernelGGL(k_swiglu_bwd_q8, dim3((unsigned)grid), dim3(kQ8Threads), 0, stream,
                      reinterpret_cast<const q8_u32x2*>(h13q), h13scale,
                      reinterpret_cast<const u32x4*>(dact), reinterpret_cast<u32x4*>(dh13),
-                     reinterpret_cast<u32x4*>(act), rows, cfg->Hp / 8);
+                     reinterpret_cast<u32x4*>(act), rows, hv, per);
   return hip_status();
 }
 
@@ -368,16 +388,17 @@ extern "C" int moe_combine_backward_q8(const moe_cfg* cfg, const moe_plan* plan,
     return MOE_EINVAL;
   if (!aligned16(dout, dy) || !aligned16(yq) || !aligned16(gates, dgates)) return MOE_EINVAL;
   const int hv = cfg->Hp / 8;
-  const int cu = (hv + 255) / 256;                       // vectors per thread, one pass
-  const dim3 grid(ntok), block(256);
+  const dim3 block(256);
   const u32x4* ds = reinterpret_cast<const u32x4*>(dout);
   const q8_u32x2* ysrc = reinterpret_cast<const q8_u32x2*>(yq);
   u32x4* dd = reinterpret_cast<u32x4*>(dy);
-#define MOE_COMBINE_BWD(N)                                                                   \
-  hipLaunchKernelGGL((k_combine_bwd_q8<N, 8>), grid, block, 0, stream, ds, ysrc, yscale, gates, \
-                     plan->route, dd, dgates, cfg->K, hv)
-  if (cu <= 1) MOE_COMBINE_BWD(1);
-  else MOE_COMBINE_BWD(2);                             // larger rows take several passes
+#define MOE_COMBINE_BWD(W, N)                                                                  \
+  hipLaunchKernelGGL((k_combine_bwd_q8<W, N, 8>), dim3(W == 1 ? (ntok + 3) / 4 : ntok), block, 0, \
+                     stream, ds, ysrc, yscale, gates, plan->route, dd, dgates, ntok, cfg->K, hv)
+  if (hv <= 64) MOE_COMBINE_BWD(1, 1);
+  else if (hv <= 128) MOE_COMBINE_BWD(1, 2);
+  else if (hv <= 256) MOE_COMBINE_BWD(4, 1);
+  else MOE_COMBINE_BWD(4, 2);                          // larger rows take several passes
 #undef MOE_COMBINE_BWD
   return hip_status();
 }
