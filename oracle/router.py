@@ -35,6 +35,12 @@ def scores(z, score):
         return s, np.where(total == 0, 0.0, e / np.where(total == 0, 1.0, total))
 
 
+def complement(z):
+    """1 - sigmoid(z), not as a difference: from z = 37 on the sigmoid is 1 in float64."""
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(np.asarray(z, np.float64)))
+
+
 def choose(z, bias, K, score):
     """The K largest of z, or of s + bias; equal ones in ascending id; masked ones behind,
     NaN last."""
@@ -92,7 +98,7 @@ def backward(z, ids, score, renorm, scale, dgates=None, cu=None, counts=None, dl
             r = slice(cu[q], cu[q + 1])
             u = dloss[q] * E * counts[q] / (K * L * float(L))
             mean = p[r] @ u
-            f = p[r] * ((1 - s[r]) if score == SIGMOID else 1.0)
+            f = p[r] * (complement(z[r]) if score == SIGMOID else 1.0)
             dz[r] += f * (u - mean[:, None])
             size[r] += f * (np.abs(u) + (p[r] @ np.abs(u))[:, None])
     if dgates is not None:
@@ -107,8 +113,7 @@ def backward(z, ids, score, renorm, scale, dgates=None, cu=None, counts=None, dl
             d = w * (dg - (dg * w).sum(1, keepdims=True))
             a = w * (np.abs(dg) + (np.abs(dg) * w).sum(1, keepdims=True))
             if score == SIGMOID:
-                with np.errstate(over="ignore"):
-                    co = 1.0 / (1.0 + np.exp(zk))
+                co = complement(zk)
                 d, a = d * co, a * co
             np.add.at(dz, (t, at), np.where(ok, d, 0.0))
             np.add.at(size, (t, at), np.where(ok, a, 0.0))
@@ -120,6 +125,7 @@ def backward(z, ids, score, renorm, scale, dgates=None, cu=None, counts=None, dl
                 dz += s * (full - (full * s).sum(1, keepdims=True))
                 size += s * (mag + (mag * s).sum(1, keepdims=True))
             else:
-                dz += full * s * (1 - s)
-                size += mag * s * (1 - s)
+                co = complement(z)
+                dz += full * s * co
+                size += mag * s * co
     return dz, size
