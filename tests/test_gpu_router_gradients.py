@@ -100,3 +100,31 @@ def test_masks_in_wide_rows(E, K, score, bf16):
             strict(z, got, want, size, score, bf16)
             assert np.all(got[1] == 0)                       # a row of nothing has no gradient
             assert np.all(got[z == -np.inf] == 0)            # nor has a masked expert
+
+
+@TYPES
+@SCORES
+@pytest.mark.parametrize("E", [7, 384])
+def test_in_place(E, score, bf16):
+    """dlogits over logits, bit for bit as apart: gates, loss and both, with rows that take the
+    path for far logits."""
+    K, n = 3, 2
+    zt = torch.from_numpy(np.concatenate([hard_rows(E, K, E), hard_rows(E, K, E + 1)]))
+    zt = zt.to(torch.bfloat16) if bf16 else zt
+    z, T = zt.double().numpy(), zt.shape[0]
+    c = R.cfg_of(1, T, E, K)
+    g = np.random.default_rng(E)
+    ids = O.choose(z, None, K, score)
+    cu = np.array([1, 9, T - 2], np.int32)
+    counts = R.on_gpu(O.balance(z, ids, cu, score)[0], torch.int32)
+    ids, cu = R.on_gpu(ids, torch.int32), R.on_gpu(cu, torch.int32)
+    dg, dl = R.on_gpu(g.standard_normal((T, K)), torch.float32), R.on_gpu(g.standard_normal(n), torch.float32)
+    for renorm in (0, 1):
+        rc = mx.make_router_cfg(score, renorm, 2.0, bf16, n)
+        for args in ((ids, dg, cu, counts, dl), (ids, dg, None, None, None),
+                     (None, None, cu, counts, dl)):
+            want = R.run_backward(c, rc, zt.cuda(), *args)
+            zg = zt.cuda()
+            mx.moe_router_backward(c, rc, zg, *args, zg)
+            torch.cuda.synchronize()
+            assert np.array_equal(zg.double().cpu().numpy(), want)
