@@ -511,7 +511,8 @@ int moe_balance_loss(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void 
  *              + dloss[q] d loss[q] / d z
  * The choice of experts and the counts are constants.  Written whole, rounded
  * once, in the logits' type; a token of no sequence has no second part.  An id
- * outside [0, E) contributes nothing.  dlogits may be logits (in place) and
+ * outside [0, E) contributes nothing; one named twice by a token is two gates,
+ * each with its share of the renormalising sum.  dlogits may be logits (in place) and
  * must not overlap it otherwise.
  * topk_ids is read only with dgates, counts and cu_tokens only with dloss; at
  * least one of dgates and dloss is given.

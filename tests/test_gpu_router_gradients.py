@@ -128,3 +128,25 @@ def test_in_place(E, score, bf16):
             mx.moe_router_backward(c, rc, zg, *args, zg)
             torch.cuda.synchronize()
             assert np.array_equal(zg.double().cpu().numpy(), want)
+
+
+@TYPES
+@SCORES
+def test_expert_named_twice(score, bf16):
+    """Each naming is a gate of its own; their parts add at the expert's logit."""
+    T, E, K = 40, 30, 6
+    g = np.random.default_rng(12)
+    zt, z = R.make_logits(T, E, bf16, 13)
+    ids = g.integers(0, E, (T, K)).astype(np.int32)
+    ids[:, 1] = ids[:, 0]
+    ids[:10, 3:] = ids[:10, :1]                             # five of six the same
+    ids[10:20] = ids[10:20, :1]                             # all the same
+    ids[20:25, 2] = -1
+    c = R.cfg_of(1, T, E, K)
+    dg = g.standard_normal((T, K)).astype(np.float32)
+    for renorm in (0, 1):
+        rc = mx.make_router_cfg(score, renorm, 1.5, bf16, 1)
+        want, size = O.backward(z, ids, score, bool(renorm), 1.5, dg)
+        got = R.run_backward(c, rc, zt.cuda(), R.on_gpu(ids, torch.int32),
+                             R.on_gpu(dg, torch.float32), None, None, None)
+        strict(z, got, want, size, score, bf16)
