@@ -472,9 +472,12 @@ int moe_router_workspace_size(const moe_cfg *cfg, const moe_router_cfg *rcfg, si
  *                 only.
  * bias [E] fp32 or NULL, topk_ids [R*S][K] int32 and gates [R*S][K] fp32 as
  * moe_plan_run and moe_combine take them.  A logit of -inf masks an expert:
- * its score is 0 and it is chosen after all others, whatever its bias; a row of
- * nothing else gets the lowest ids and gates of 0.  A NaN logit is chosen last of all; NaN and
- * +inf pass through the sums they enter as IEEE arithmetic has it.
+ * its score is 0 and it is chosen after all others, whatever its bias or
+ * theirs; a row of nothing else gets the lowest ids and gates of 0.  A NaN logit
+ * is chosen last of all, after the masked ones.  NaN and +inf pass through the
+ * sums they enter as IEEE arithmetic has it: experts whose sum with the bias is
+ * NaN (a NaN bias; all of a softmax row with NaN or +inf in it) are chosen after
+ * those that have a number, before masked ones, in ascending id.
  *
  * Balance loss (with counts, prob and loss given; all three or none).  Tokens
  * cu_tokens[q] .. cu_tokens[q + 1] - 1 are sequence q, 0 <= q < nseq

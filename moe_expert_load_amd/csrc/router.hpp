@@ -464,9 +464,10 @@ __device__ __forceinline__ int order64(const RouterArgs& a, int64_t at, float mf
 }
 
 // take_top on the float64 scores plus bias: the K largest, equal ones in
-// ascending expert, NaN last.  For rows that nothing else orders (NaN, more
-// than 64 keys near each other), so nothing is kept in registers between
-// rounds: the scores are computed anew.
+// ascending expert; after all numbers the sums that are NaN (a NaN bias, a softmax
+// row with NaN or +inf), then the masked experts, NaN logits last, each of these
+// in ascending expert.  For rows that nothing else orders, so nothing is kept in
+// registers between rounds: the scores are computed anew.
 template <bool BF16, bool SOFT>
 __device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float mf) {
   const int lane = lane_id();
@@ -474,15 +475,16 @@ __device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float
   uint32_t taken = 0;                            // at most 32 experts a lane
   int mine = 0;
   for (int k = 0; k < a.K; ++k) {
-    // class of a candidate: 2 a number, 1 NaN, 0 none
+    // class of a candidate: 4 a number, 3 NaN, 2 masked, 1 a NaN logit, 0 none
     double best = 0.0;
     int cls = 0, id = 0x7fffffff;
 #pragma unroll 1
     for (int i = 0, e = lane; e < a.E; ++i, e += kWave) {
       if (taken >> i & 1) continue;
+      const float z = logit_at<BF16>(a.logits, at + e);
       const double d = key64<BF16, SOFT>(a, at, e, m, sum);
-      const int c = d == d ? 2 : 1;
-      if (c > cls || (c == cls && c == 2 && d > best)) {
+      const int c = z != z ? 1 : z == -INFINITY ? 2 : d == d ? 4 : 3;
+      if (c > cls || (c == cls && c == 4 && d > best)) {
         cls = c;
         best = d;
         id = e;
@@ -492,8 +494,8 @@ __device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float
     for (int o = 32; o > 0; o >>= 1) {
       const double od = __shfl_xor(best, o, kWave);
       const int oc = __shfl_xor(cls, o, kWave), oi = __shfl_xor(id, o, kWave);
-      const bool equal = oc == cls && (cls < 2 || od == best);
-      if (oc > cls || (oc == cls && cls == 2 && od > best) || (equal && oi < id)) {
+      const bool equal = oc == cls && (cls < 4 || od == best);
+      if (oc > cls || (oc == cls && cls == 4 && od > best) || (equal && oi < id)) {
         best = od;
         cls = oc;
         id = oi;

@@ -42,15 +42,15 @@ def complement(z):
 
 
 def choose(z, bias, K, score):
-    """The K largest of z, or of s + bias; equal ones in ascending id; masked ones behind,
-    NaN last."""
+    """The K largest of z, or of s + bias; equal ones in ascending id.  Sums that are NaN come
+    after numbers, masked experts (-inf) after those, NaN logits last, each in ascending id."""
     z = np.asarray(z, np.float64)
     key = z
-    if bias is not None:                               # a logit of -inf masks its expert
-        key = np.where(z == -np.inf, -np.inf, scores(z, score)[0] + np.asarray(bias, np.float64))
-    nan = np.isnan(key)
+    if bias is not None:
+        key = scores(z, score)[0] + np.asarray(bias, np.float64)
+    kind = np.where(np.isnan(z), 3, np.where(z == -np.inf, 2, np.where(np.isnan(key), 1, 0)))
     order = np.lexsort((np.broadcast_to(np.arange(z.shape[1]), z.shape),
-                        -np.where(nan, -np.inf, key), nan), axis=1)
+                        np.where(kind == 0, -key, 0.0), kind), axis=1)
     return order[:, :K].astype(np.int32)
 
 
