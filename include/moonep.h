@@ -556,7 +556,8 @@ int moe_q8_load(int64_t rows, int32_t width, const uint8_t *q, const uint8_t *sc
 /*
  * moe_dispatch of a layer input kept in 8 bits: xperm[route[t*K + k]] = the
  * values of row t of (xq, xscale), bit for bit those of moe_q8_load.  xq
- * [R*S][H], xscale [R*S][ceil(H/32)] as moe_q8_store(R*S, H, ...) writes them.
+ * [R*S][H], xscale [R*S][ceil(H/32)] as moe_q8_store(R*S, H, ...) writes them;
+ * xperm must not overlap them.
  */
 int moe_dispatch_q8(const moe_cfg *cfg, const moe_plan *plan, const uint8_t *xq,
                     const uint8_t *xscale, moe_bf16 *xperm, hipStream_t stream);

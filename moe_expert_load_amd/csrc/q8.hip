@@ -337,6 +337,9 @@ extern "C" int moe_dispatch_q8(const moe_cfg* cfg, const moe_plan* plan, const u
   if (!plan || !plan->route || !xq || !xscale || !xperm) return MOE_EINVAL;
   if (!aligned16(xq, xperm)) return MOE_EINVAL;
   const int hv = cfg->H / 8;
+  const int64_t n = int64_t(ntok) * cfg->H;
+  if (clash({{xperm, 2 * n * cfg->K}}, {{xq, n}, {xscale, int64_t(ntok) * ((hv + 3) / 4)}}))
+    return MOE_EINVAL;
   const int q = (hv + 4 * kWave - 1) / (4 * kWave);
   const dim3 grid(ntok), block(256);
   const q8_u32x2* xs = reinterpret_cast<const q8_u32x2*>(xq);

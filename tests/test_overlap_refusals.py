@@ -1,0 +1,53 @@
+"""Tensors that share memory with an output are refused before any launch (CPU).
+
+Addresses are made up; a call that passed the checks would launch, so every call here is one
+that must be refused: the output reaches one byte, or one aligned step, into its neighbour.
+"""
+import ctypes
+import os
+
+import pytest
+
+import moe_expert_load_amd as mx
+
+R, S, E, K, H, Hp, B = 4, 16, 8, 2, 128, 64, 2         # 64 tokens, 128 rows
+T, ROWS = R * S, R * S * K
+CFG = mx.make_cfg(R, S, E, K, H, Hp, B)
+PLAN = mx.moe_plan(*[ctypes.c_void_p(1 << 24) for _ in mx.PLAN_FIELDS])
+FAR = 1 << 32
+GAP = 1 << 28
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(mx.LIB_PATH):
+        from moe_expert_load_amd import build
+        build.build()
+    return mx.load()
+
+
+def refused(call, sizes, pairs, step=16):
+    """call(addresses) is refused whenever a pair (written, other) of `sizes`' tensors shares
+    its first or its last bytes; the other tensors lie far apart."""
+    order = list(sizes)
+    base = {n: FAR + i * GAP for i, n in enumerate(order)}
+    for w, o in pairs:
+        for at in (base[o], base[o] + sizes[o] - 1 & -step, base[o] - sizes[w] + step & -step):
+            a = dict(base)
+            a[w] = at
+            assert at < base[o] + sizes[o] and base[o] < at + sizes[w]
+            assert call(a) == mx.MOE_EINVAL, (w, o, at - base[o])
+
+
+def pointer(a):
+    return {k: ctypes.c_void_p(v) for k, v in a.items()}
+
+
+def test_dispatch_q8(lib):
+    sizes = {"xq": T * H, "xscale": T * H // 32, "xperm": ROWS * H * 2}
+
+    def call(a):
+        p = pointer(a)
+        return lib.moe_dispatch_q8(ctypes.byref(CFG), ctypes.byref(PLAN), p["xq"], p["xscale"],
+                                   p["xperm"], None)
+    refused(call, sizes, [("xperm", "xq"), ("xperm", "xscale")])
