@@ -589,7 +589,9 @@ int moe_swiglu_backward_q8(const moe_cfg *cfg, const uint8_t *h13q, const uint8_
 
 /*
  * moe_combine_backward from y kept in 8 bits (moe_q8_store(R*S*K, H', y,
- * ...)): dy as there, dgates with the values that the codes stand for.
+ * ...)): dy as there, dgates with the values that the codes stand for.  dy and
+ * dgates must not overlap the inputs or each other, except that dgates may be
+ * gates (in place).
  */
 int moe_combine_backward_q8(const moe_cfg *cfg, const moe_plan *plan, const moe_bf16 *dout,
                             const uint8_t *yq, const uint8_t *yscale, const float *gates,

@@ -391,6 +391,12 @@ extern "C" int moe_combine_backward_q8(const moe_cfg* cfg, const moe_plan* plan,
     return MOE_EINVAL;
   if (!aligned16(dout, dy) || !aligned16(yq) || !aligned16(gates, dgates)) return MOE_EINVAL;
   const int hv = cfg->Hp / 8;
+  const int64_t rows = int64_t(ntok) * cfg->K, n = rows * cfg->Hp;
+  const Range in[] = {{dout, 2 * int64_t(ntok) * cfg->Hp}, {yq, n}, {yscale, rows * ((hv + 3) / 4)}};
+  // a token's gates are read before its dgates are written: in place is fine
+  if (clash({{dy, 2 * n}, {dgates, 4 * rows}}, in) || overlap(dy, 2 * n, gates, 4 * rows) ||
+      (dgates != gates && overlap(dgates, 4 * rows, gates, 4 * rows)))
+    return MOE_EINVAL;
   const dim3 block(256);
   const u32x4* ds = reinterpret_cast<const u32x4*>(dout);
   const q8_u32x2* ysrc = reinterpret_cast<const q8_u32x2*>(yq);

@@ -51,3 +51,18 @@ def test_dispatch_q8(lib):
         return lib.moe_dispatch_q8(ctypes.byref(CFG), ctypes.byref(PLAN), p["xq"], p["xscale"],
                                    p["xperm"], None)
     refused(call, sizes, [("xperm", "xq"), ("xperm", "xscale")])
+
+
+def test_combine_backward_q8(lib):
+    sizes = {"dout": T * Hp * 2, "yq": ROWS * Hp, "yscale": ROWS * Hp // 32, "gates": ROWS * 4,
+             "dy": ROWS * Hp * 2, "dgates": ROWS * 4}
+
+    def call(a):
+        p = pointer(a)
+        if p["dgates"].value == p["gates"].value:           # in place is allowed
+            return mx.MOE_EINVAL
+        return lib.moe_combine_backward_q8(ctypes.byref(CFG), ctypes.byref(PLAN), p["dout"],
+                                           p["yq"], p["yscale"], p["gates"], p["dy"], p["dgates"],
+                                           None)
+    ins = ("dout", "yq", "yscale", "gates")
+    refused(call, sizes, [(w, o) for w in ("dy", "dgates") for o in ins] + [("dy", "dgates")])
