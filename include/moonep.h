@@ -567,7 +567,9 @@ int moe_dispatch_q8(const moe_cfg *cfg, const moe_plan *plan, const uint8_t *xq,
  * h13q [R][S*K][2H'] and h13scale [R][S*K][2][ceil(H'/32)] are bit for bit
  * what moe_q8_store(2*R*S*K, H', h13, ...) makes of that call's h13 (gate and
  * up have blocks of their own).  act as there.  Rows outside the listed ranks
- * are not written.
+ * are not written.  The listed ranks' rows of act, h13q and h13scale and the
+ * workspace must not overlap each other, the weights, or those ranks' rows of
+ * xperm and cu_seqlens.
  */
 int moe_grouped_gemm_swiglu_q8(const moe_cfg *cfg, const moe_bf16 *xperm,
                                const moe_bf16 *w13_home, const moe_bf16 *w13_pref,

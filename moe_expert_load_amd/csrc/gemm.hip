@@ -53,6 +53,7 @@
 
 #include "common.hpp"
 #include "host.hpp"
+#include "overlap.hpp"
 #include "q8.hpp"
 
 namespace moonep {
@@ -1689,6 +1690,22 @@ static int swiglu_projection(const moe_cfg* cfg, const moe_bf16* xperm, const mo
   if (cfg->B > 0 && !w13_pref) return MOE_EINVAL;
   if (q8 && (!h13q || !h13s || !aligned16(h13q))) return MOE_EINVAL;
   if (!aligned16(xperm, w13_home, w13_pref, act, h13, workspace)) return MOE_EINVAL;
+  if (q8) {                                        // the listed ranks' parts of every tensor
+    const int64_t first = int64_t(rank_begin) * cfg->S * cfg->K, nr = rank_end - rank_begin;
+    const int64_t rows = nr * cfg->S * cfg->K, wide = 2 * int64_t(cfg->Hp);
+    const int64_t sb = 2 * ((int64_t(cfg->Hp) + kQ8Block - 1) / kQ8Block), segs = cfg->E + cfg->B;
+    const int64_t w = int64_t(cfg->H) * wide * 2;
+    if (clash({{act + first * cfg->Hp, rows * cfg->Hp * 2},
+               {h13q + first * wide, rows * wide},
+               {h13s + first * sb, rows * sb},
+               {workspace, (int64_t)gemm_ws_bytes(cfg)}},
+              {{xperm + first * cfg->H, rows * cfg->H * 2},
+               {w13_home, cfg->E * w},
+               {cfg->B > 0 ? w13_pref + int64_t(rank_begin) * cfg->B * (w / 2) : nullptr,
+                nr * cfg->B * w},
+               {cu_seqlens + rank_begin * (segs + 1), nr * (segs + 1) * 4}}))
+      return MOE_EINVAL;
+  }
   GemmArgs g{};
   g.xperm = xperm; g.w_home = w13_home; g.w_pref = w13_pref; g.y = act; g.h13 = h13;
   g.h13q = h13q; g.h13s = h13s;

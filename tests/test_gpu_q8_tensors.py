@@ -77,3 +77,36 @@ def test_dispatch_side_by_side():
     mx.moe_dispatch_q8(c, plan, q, s, xp)
     torch.cuda.synchronize()
     assert torch.equal(xp.view(torch.int16), want.view(torch.int16).reshape(-1))
+
+
+def test_projection_over_another_ranks_rows():
+    """Rank 1's act may lie where rank 0's rows of xperm were; the other tensors side by side."""
+    shape = W.TINY.with_(H=72, Hp=40, S=37)
+    c, _ = cfgs(shape)
+    ids, _ = W.routing_uniform(shape, salt=8)
+    plan, _ = gpu_plan(shape, ids)
+    rows, n, H, Hp, bf = shape.R * shape.SK, shape.SK, shape.H, shape.Hp, torch.bfloat16
+    nb = Q.blocks(Hp)
+    c13 = mx.make_cfg(shape.R, shape.S, shape.E, shape.K, H, 2 * Hp, shape.B, shape.mode)
+    x = W.randn_bf16((shape.tokens, H), 1, "cuda")
+    w = W.randn_bf16((shape.E, H, 2 * Hp), 2, "cuda")
+    wp = torch.zeros((shape.R * shape.B, H, 2 * Hp), dtype=bf, device="cuda")
+    ws0 = torch.empty(mx.moe_gemm_workspace_size(c), dtype=torch.uint8, device="cuda")
+    mx.moe_prefetch_weight(c13, plan, w, wp)
+    xp0 = torch.zeros((rows, H), dtype=bf, device="cuda")
+    mx.moe_dispatch(c, plan, x, xp0)
+    act0, q0, s0 = (torch.zeros(rows * Hp, dtype=bf, device="cuda"),
+                    torch.zeros(rows * 2 * Hp, dtype=torch.uint8, device="cuda"),
+                    torch.zeros(rows * 2 * nb, dtype=torch.uint8, device="cuda"))
+    mx.moe_grouped_gemm_swiglu_q8(c, xp0, w, wp, plan.cu_seqlens, act0, q0, s0, 0, shape.R, ws0)
+    both, q, ws, s = side_by_side((n * Hp + rows * H, bf), (rows * 2 * Hp, torch.uint8),
+                                  (ws0.numel(), torch.uint8), (rows * 2 * nb, torch.uint8))
+    xp, act = both[n * Hp:], both[:rows * Hp]
+    assert n * Hp * 2 % 16 == 0 and Hp <= H
+    xp.copy_(xp0.reshape(-1))
+    mx.moe_grouped_gemm_swiglu_q8(c, xp, w, wp, plan.cu_seqlens, act, q, s, 1, 2, ws)
+    torch.cuda.synchronize()
+    part = slice(n * Hp, 2 * n * Hp)
+    assert torch.equal(act[part].view(torch.int16), act0[part].view(torch.int16))
+    assert torch.equal(q[n * 2 * Hp:2 * n * 2 * Hp], q0[n * 2 * Hp:2 * n * 2 * Hp])
+    assert torch.equal(s[n * 2 * nb:2 * n * 2 * nb], s0[n * 2 * nb:2 * n * 2 * nb])

@@ -66,3 +66,32 @@ def test_combine_backward_q8(lib):
                                            None)
     ins = ("dout", "yq", "yscale", "gates")
     refused(call, sizes, [(w, o) for w in ("dy", "dgates") for o in ins] + [("dy", "dgates")])
+
+
+def swiglu_q8(lib, begin, end):
+    def call(a):
+        p = pointer(a)
+        return lib.moe_grouped_gemm_swiglu_q8(
+            ctypes.byref(CFG), *[p[n] for n in ("xperm", "home", "pref", "cu", "act", "q", "s")],
+            begin, end, p["ws"], None)
+    return call
+
+
+def test_grouped_gemm_swiglu_q8(lib):
+    sizes = {"xperm": ROWS * H * 2, "home": E * H * 2 * Hp * 2, "pref": R * B * H * 2 * Hp * 2,
+             "cu": R * (E + B + 1) * 4, "act": ROWS * Hp * 2, "q": ROWS * 2 * Hp,
+             "s": ROWS * 2 * (Hp // 32), "ws": mx.moe_gemm_workspace_size(CFG)}
+    outs = ("act", "q", "s", "ws")
+    pairs = [(w, o) for w in outs for o in ("xperm", "home", "pref", "cu")]
+    pairs += [(w, o) for i, w in enumerate(outs) for o in outs[:i]]
+    refused(swiglu_q8(lib, 0, R), sizes, pairs)
+
+
+def test_grouped_gemm_swiglu_q8_of_one_rank(lib):
+    """Only the listed rank's parts count: act may start where that rank's rows of xperm end,
+    and not 16 bytes before."""
+    n = ROWS // R
+    a = {k: FAR + i * GAP for i, k in enumerate(("xperm", "home", "pref", "cu", "act", "q", "s", "ws"))}
+    first = a["xperm"] + n * H * 2                          # rank 1's rows of xperm
+    for at in (first - n * Hp * 2 + 16, first, first + n * H * 2 - 16):
+        assert swiglu_q8(lib, 1, 2)({**a, "act": at - n * Hp * 2}) == mx.MOE_EINVAL
