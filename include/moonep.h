@@ -491,7 +491,7 @@ int moe_router_workspace_size(const moe_cfg *cfg, const moe_router_cfg *rcfg, si
  * part in the loss.  A row of -inf alone has p = 0.  The sums run in a fixed
  * order: the same inputs give bit-identical outputs.  workspace (only with the
  * loss): moe_router_workspace_size() bytes; concurrent calls need distinct
- * ones.
+ * ones.  Outputs and workspace must not overlap each other or the inputs.
  */
 int moe_router(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
                const float *bias, int32_t *topk_ids, float *gates, const int32_t *cu_tokens,
@@ -500,7 +500,7 @@ int moe_router(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logit
 /*
  * The balance loss of moe_router for given topk_ids [R*S][K] (a router of the
  * caller's own).  An id outside [0, E) is not counted; one named twice by a
- * token counts twice.
+ * token counts twice.  Overlap as for moe_router.
  */
 int moe_balance_loss(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
                      const int32_t *topk_ids, const int32_t *cu_tokens, int32_t *counts,

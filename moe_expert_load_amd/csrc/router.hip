@@ -330,6 +330,24 @@ inline int check_router(const moe_cfg* c, const moe_router_cfg* r) {
   return MOE_OK;
 }
 
+inline size_t router_ws_bytes(const moe_cfg* c, int nseq) {
+  const int T = c->R * c->S;
+  return align256((part_rows(T, nseq) * 8 + sum_rows(T, nseq) * 12) * c->E);
+}
+
+// Whether a forward call's outputs share memory with what it reads or each other.
+// ids and gates are null where they are not written; loss is null without one.
+inline bool forward_clash(const moe_cfg* c, const moe_router_cfg* r, const RouterArgs& a,
+                          const int32_t* ids_in, const int32_t* counts, const float* prob,
+                          const float* loss, const void* workspace) {
+  const int64_t T = int64_t(c->R) * c->S, row = int64_t(r->nseq) * c->E * 4, k = T * c->K * 4;
+  const int64_t ws = loss ? (int64_t)router_ws_bytes(c, r->nseq) : 0;
+  return clash({{ids_in ? nullptr : a.ids, k}, {a.gates, k}, {counts, row}, {prob, row},
+                {loss, int64_t(r->nseq) * 4}, {workspace, ws}},
+               {{a.logits, T * c->E * (r->logits_bf16 ? 2 : 4)}, {a.bias, int64_t(c->E) * 4},
+                {ids_in, k}, {loss ? a.cu : nullptr, (int64_t(r->nseq) + 1) * 4}});
+}
+
 inline int run_forward(const moe_cfg* c, const moe_router_cfg* r, RouterArgs a, bool select,
                        int32_t* counts, float* prob, float* loss, void* workspace,
                        hipStream_t stream) {
@@ -391,9 +409,7 @@ extern "C" int moe_router_workspace_size(const moe_cfg* cfg, const moe_router_cf
   const int rc = check_router(cfg, rcfg);
   if (rc != MOE_OK) return rc;
   if (!bytes_out) return MOE_EINVAL;
-  const int T = cfg->R * cfg->S;
-  *bytes_out =
-      align256((part_rows(T, rcfg->nseq) * 8 + sum_rows(T, rcfg->nseq) * 12) * cfg->E);
+  *bytes_out = router_ws_bytes(cfg, rcfg->nseq);
   return MOE_OK;
 }
 
@@ -415,6 +431,7 @@ extern "C" int moe_router(const moe_cfg* cfg, const moe_router_cfg* rcfg, const 
   a.ids = topk_ids;
   a.gates = gates;
   a.cu = cu_tokens;
+  if (forward_clash(cfg, rcfg, a, nullptr, counts, prob, loss, workspace)) return MOE_EINVAL;
   return run_forward(cfg, rcfg, a, true, counts, prob, loss, workspace, stream);
 }
 
@@ -431,6 +448,7 @@ extern "C" int moe_balance_loss(const moe_cfg* cfg, const moe_router_cfg* rcfg, 
   a.logits = logits;
   a.ids = const_cast<int32_t*>(topk_ids);
   a.cu = cu_tokens;
+  if (forward_clash(cfg, rcfg, a, topk_ids, counts, prob, loss, workspace)) return MOE_EINVAL;
   return run_forward(cfg, rcfg, a, false, counts, prob, loss, workspace, stream);
 }
 

@@ -95,3 +95,48 @@ def test_grouped_gemm_swiglu_q8_of_one_rank(lib):
     first = a["xperm"] + n * H * 2                          # rank 1's rows of xperm
     for at in (first - n * Hp * 2 + 16, first, first + n * H * 2 - 16):
         assert swiglu_q8(lib, 1, 2)({**a, "act": at - n * Hp * 2}) == mx.MOE_EINVAL
+
+
+NSEQ = 3
+LOSS = {"logits": T * E * 4, "bias": E * 4, "ids": T * K * 4, "gates": T * K * 4,
+        "cu": (NSEQ + 1) * 4, "counts": NSEQ * E * 4, "prob": NSEQ * E * 4, "loss": NSEQ * 4}
+
+
+def settings():
+    return mx.make_router_cfg(mx.SCORE_SOFTMAX, 1, 1.0, False, NSEQ)
+
+
+def pairs_of(outs, ins):
+    return [(w, o) for w in outs for o in ins] + [(w, o) for i, w in enumerate(outs) for o in outs[:i]]
+
+
+def test_router(lib):
+    rc = settings()
+    sizes = {**LOSS, "ws": mx.moe_router_workspace_size(CFG, rc)}
+
+    def loss(a):
+        p = pointer(a)
+        return lib.moe_router(ctypes.byref(CFG), ctypes.byref(rc),
+                              *[p[n] for n in ("logits", "bias", "ids", "gates", "cu", "counts",
+                                               "prob", "loss", "ws")], None)
+
+    def plain(a):
+        p = pointer(a)
+        return lib.moe_router(ctypes.byref(CFG), ctypes.byref(rc),
+                              *[p[n] for n in ("logits", "bias", "ids", "gates")], *[None] * 6)
+
+    outs = ("ids", "gates", "counts", "prob", "loss", "ws")
+    refused(loss, sizes, pairs_of(outs, ("logits", "bias", "cu")))
+    refused(plain, sizes, pairs_of(("ids", "gates"), ("logits", "bias")))
+
+
+def test_balance_loss(lib):
+    rc = settings()
+    sizes = {**LOSS, "ws": mx.moe_router_workspace_size(CFG, rc)}
+
+    def call(a):
+        p = pointer(a)
+        return lib.moe_balance_loss(ctypes.byref(CFG), ctypes.byref(rc),
+                                    *[p[n] for n in ("logits", "ids", "cu", "counts", "prob", "loss",
+                                                     "ws")], None)
+    refused(call, sizes, pairs_of(("counts", "prob", "loss", "ws"), ("logits", "ids", "cu")))
