@@ -515,10 +515,10 @@ int moe_balance_loss(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void 
  * The choice of experts and the counts are constants.  Written whole, rounded
  * once, in the logits' type; a token of no sequence has no second part.  An id
  * outside [0, E) contributes nothing; one named twice by a token is two gates,
- * each with its share of the renormalising sum.  dlogits may be logits (in place) and
- * must not overlap it otherwise.
+ * each with its share of the renormalising sum.
  * topk_ids is read only with dgates, counts and cu_tokens only with dloss; at
- * least one of dgates and dloss is given.
+ * least one of dgates and dloss is given.  dlogits may be logits (in place); it
+ * must not overlap them otherwise, nor anything else that is read.
  */
 int moe_router_backward(const moe_cfg *cfg, const moe_router_cfg *rcfg, const void *logits,
                         const int32_t *topk_ids, const float *dgates, const int32_t *cu_tokens,

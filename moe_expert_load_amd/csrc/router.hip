@@ -467,6 +467,12 @@ extern "C" int moe_router_backward(const moe_cfg* cfg, const moe_router_cfg* rcf
     return MOE_EINVAL;
   const int64_t bytes = int64_t(cfg->R) * cfg->S * cfg->E * (rcfg->logits_bf16 ? 2 : 4);
   if (dlogits != logits && overlap(logits, bytes, dlogits, bytes)) return MOE_EINVAL;
+  const int64_t k = int64_t(cfg->R) * cfg->S * cfg->K * 4, n = rcfg->nseq;
+  if (clash({{dlogits, bytes}},
+            {{dgates ? topk_ids : nullptr, k}, {dgates, k}, {dloss, n * 4},
+             {dloss ? cu_tokens : nullptr, (n + 1) * 4},
+             {dloss ? counts : nullptr, n * cfg->E * 4}}))
+    return MOE_EINVAL;
   RouterArgs a{};
   a.logits = logits;
   a.ids = const_cast<int32_t*>(topk_ids);

@@ -140,3 +140,26 @@ def test_balance_loss(lib):
                                     *[p[n] for n in ("logits", "ids", "cu", "counts", "prob", "loss",
                                                      "ws")], None)
     refused(call, sizes, pairs_of(("counts", "prob", "loss", "ws"), ("logits", "ids", "cu")))
+
+
+def test_router_backward(lib):
+    rc = settings()
+    sizes = {**LOSS, "dgates": T * K * 4, "dloss": NSEQ * 4, "dlogits": T * E * 4}
+
+    def call(names):
+        def f(a):
+            p = {**pointer(a), None: None}
+            return lib.moe_router_backward(ctypes.byref(CFG), ctypes.byref(rc), p["logits"],
+                                           *[p[n] for n in names], p["dlogits"], None)
+        return f
+
+    both = ("ids", "dgates", "cu", "counts", "dloss")
+    refused(call(both), sizes, pairs_of(("dlogits",), both))
+    refused(call(("ids", "dgates", None, None, None)), sizes,
+            pairs_of(("dlogits",), ("ids", "dgates")))
+    refused(call((None, None, "cu", "counts", "dloss")), sizes,
+            pairs_of(("dlogits",), ("cu", "counts", "dloss")))
+    # logits: shifted by a step either way (in place is allowed)
+    base = {n: FAR + i * GAP for i, n in enumerate(sizes)}
+    for off in (16, -16, sizes["logits"] - 16, 16 - sizes["logits"]):
+        assert call(both)({**base, "dlogits": base["logits"] + off}) == mx.MOE_EINVAL
