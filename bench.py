@@ -99,11 +99,26 @@ def _code_only(text):
     return " ".join(text.split())
 
 
+def kernel_sources(kernel):
+    """A kernel's source and every csrc header that it includes, directly or not."""
+    import re
+    csrc = os.path.join(ROOT, "moe_expert_load_amd", "csrc")
+    todo, found = [os.path.join(ROOT, KERNEL_SOURCES[kernel])], []
+    while todo:
+        path = todo.pop(0)
+        if path in found or not os.path.exists(path):
+            continue
+        found.append(path)
+        names = re.findall(r'^#include "([^"]+)"', open(path, encoding="utf-8").read(), re.M)
+        todo += [os.path.join(csrc, n) for n in names]
+    return found
+
+
 def source_digest(kernel):
     import hashlib
     h = hashlib.sha256()
-    for rel in (KERNEL_SOURCES[kernel], "moe_expert_load_amd/csrc/common.hpp"):
-        h.update(_code_only(open(os.path.join(ROOT, rel), encoding="utf-8").read()).encode())
+    for path in kernel_sources(kernel):
+        h.update(_code_only(open(path, encoding="utf-8").read()).encode())
     return h.hexdigest()[:16]
 
 
