@@ -233,8 +233,11 @@ __device__ __forceinline__ float row_shares(const RouterArgs& a, int64_t t, cons
 
 // The K largest keys in order, equal ones in ascending expert; lane k returns
 // the k-th id.  key is consumed.  Any keys: K rounds of a maximum of the wave.
-// For rows that sort_top leaves (NaN, masks, many equal keys): used for all rows
-// of 896 experts and K = 16 it takes 1,174 us where sort_top takes 205.
+// For rows that sort_top leaves: NaN, masks, many equal keys, and with K above 24
+// ordinary rows, whose 64 lanes cannot bound so many keys (65,536 bf16 rows of 384
+// experts: routes 26 us with K = 8, 43 with 24, 70 with 28, 153 with 32, 327 with
+// 64).  Used for all rows of 896 experts and K = 16 it takes 1,174 us where
+// sort_top takes 205.
 template <int P>
 __device__ __forceinline__ int take_top(int (&key)[P], int K) {
   const int lane = lane_id();
@@ -466,8 +469,11 @@ __device__ __forceinline__ int order64(const RouterArgs& a, int64_t at, float mf
 // take_top on the float64 scores plus bias: the K largest, equal ones in
 // ascending expert; after all numbers the sums that are NaN (a NaN bias, a softmax
 // row with NaN or +inf), then the masked experts, NaN logits last, each of these
-// in ascending expert.  For rows that nothing else orders, so nothing is kept in
-// registers between rounds: the scores are computed anew.
+// in ascending expert.  For rows that sort_top leaves, K of them finite or fewer
+// among them, and for every row of K = 64 below E.  Nothing is kept in registers
+// between rounds: the scores are computed anew, K times E of them.  Ordinary rows
+// with a bias come here from K = 28 on: 65,536 of 384 experts take 40 us with
+// K = 8, 2.1 ms with 32 and 4.8 with 64; of 896, 56 us, 4.8 and 10 ms.
 template <bool BF16, bool SOFT>
 __device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float mf) {
   const int lane = lane_id();
@@ -512,13 +518,19 @@ __device__ __forceinline__ int take_top64(const RouterArgs& a, int64_t at, float
 //
 // The order is that of float64 scores plus bias; fp32 keys give it wherever
 // neighbours among the K + 1 largest keys are further apart than two keys'
-// errors.  With h = 2^-24 a key is off by
-//   sigmoid  s (1 - s) |z| 2.2 h + 2.5 ulp of s  <=  1.4e-8 + 3e-7,
-//   softmax  s (|z - shift| 2.2 h + the sum's relative error), where
-//            s |z - max| <= 0.37 p_max and the sum's error is at most
-//            (2.2 ln E + 48 + 33) h:  <= 8e-6 p_max,
-// and by h |key| from the addition.  Other rows list every key that may be
+// errors.  With h = 2^-24 a sigmoid key is off by the argument's rounding,
+//   s (1 - s) |z| 2.2 h  <=  2.9e-8,
+// and by the exponential's, the sum's and the reciprocal's, at most 2^-22 of a
+// score above 1/2 and 3 * 2^-23 of one below, 2.4e-7: 3.2e-7 covers both.  A
+// softmax key is off by
+//   s (|z - shift| 2.2 h + the sum's relative error), where
+//   s |z - max| <= 0.37 p_max and the sum's error is at most
+//   (2.2 ln E + 48 + 33) h:  <= 8e-6 p_max,
+// and both by h |key| from the addition.  Other rows list every key that may be
 // among the K largest, at most 64, and order those in float64, a lane each.
+// Equal logits under equal biases are such rows: bf16 logits with a bias of zeros
+// and the loss, 65,536 tokens, take 70 us at E = 384, K = 8 (sigmoid; with a random
+// bias 50) and 217 at E = 896, K = 16 (softmax, whose sum is taken again; 82).
 template <int P, bool BF16, bool SOFT>
 __device__ __forceinline__ int choose_biased(const RouterArgs& a, int64_t t, float m,
                                              const float (&key)[P], float inv, float shift,
