@@ -6,7 +6,7 @@ import torch
 import moe_expert_load_amd as mx
 import test_gpu_q8 as Q
 import workloads as W
-from gpu_helpers import cfgs, free, gpu_plan
+from gpu_helpers import bits, cfgs, free, gpu_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +110,54 @@ def test_projection_over_another_ranks_rows():
     assert torch.equal(act[part].view(torch.int16), act0[part].view(torch.int16))
     assert torch.equal(q[n * 2 * Hp:2 * n * 2 * Hp], q0[n * 2 * Hp:2 * n * 2 * Hp])
     assert torch.equal(s[n * 2 * nb:2 * n * 2 * nb], s0[n * 2 * nb:2 * n * 2 * nb])
+
+
+@pytest.mark.parametrize("shape", [W.TINY.with_(R=1, E=24, S=11, K=4, B=24, H=520, Hp=72),
+                                   W.SKEWED.with_(S=256, Hp=520)], ids=["few-rows", "skewed"])
+def test_projection_repeats_and_rounds_once(shape):
+    """The same bits call after call, whatever its buffers held; and every gate and up that is
+    kept is the bf16 next to the float64 product, but for the fp32 sum's own error.
+
+    A sum of H exact products in fp32 is off by H h sum |x w| at most, in any order, and its
+    rounding to bf16 by half a step, 2^-8 of the value.
+    """
+    c, _ = cfgs(shape)
+    ids, _ = W.routing_uniform(shape, salt=3)
+    plan, _ = gpu_plan(shape, ids)
+    rows, H, Hp, E = shape.R * shape.SK, shape.H, shape.Hp, shape.E
+    c13 = mx.make_cfg(shape.R, shape.S, E, shape.K, H, 2 * Hp, shape.B, shape.mode)
+    w = W.randn_bf16((E, H, 2 * Hp), 2, "cuda")
+    wp = torch.zeros((shape.R * shape.B, H, 2 * Hp), dtype=torch.bfloat16, device="cuda")
+    xp = torch.zeros((rows, H), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(mx.moe_gemm_workspace_size(c), dtype=torch.uint8, device="cuda")
+    mx.moe_prefetch_weight(c13, plan, w, wp)
+    mx.moe_dispatch(c, plan, W.randn_bf16((shape.tokens, H), 1, "cuda"), xp)
+    act = torch.empty((rows, Hp), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((rows, 2 * Hp), dtype=torch.uint8, device="cuda")
+    s = torch.empty((rows, 2 * Q.blocks(Hp)), dtype=torch.uint8, device="cuda")
+    seen = []
+    for soil in (0x00, 0xFF, 0x7F, 0x5A):
+        for t in (act.view(torch.uint8), q, s, ws):
+            t.fill_(soil)
+        mx.moe_grouped_gemm_swiglu_q8(c, xp, w, wp, plan.cu_seqlens, act, q, s, 0, shape.R, ws)
+        torch.cuda.synchronize()
+        seen.append((act.view(torch.int16).clone(), q.clone(), s.clone()))
+        assert all(torch.equal(a, b) for a, b in zip(seen[0], seen[-1]))
+    h13 = torch.zeros((rows, 2 * Hp), dtype=torch.bfloat16, device="cuda")
+    mx.moe_grouped_gemm_swiglu(c, xp, w, wp, plan.cu_seqlens, act, h13, 0, shape.R, ws)
+    q0, s0 = Q.store(bits(h13).reshape(2 * rows, Hp))
+    assert torch.equal(q.reshape(-1), q0) and torch.equal(s.reshape(-1), s0)
+    v = {k: t.cpu().numpy() for k, t in plan.views().items()}
+    cu, slot = v["cu_seqlens"].reshape(shape.R, -1), v["slot_expert"]
+    some = 0
+    for r in range(shape.R):
+        for j in range(cu.shape[1] - 1):
+            lo, hi = r * shape.SK + cu[r, j], r * shape.SK + cu[r, j + 1]
+            if hi == lo:
+                continue
+            some += 1
+            x, we = xp[lo:hi].double(), w[j if j < E else int(slot[r, j - E])].double()
+            exact, size = x @ we, x.abs() @ we.abs()
+            tol = 2.0 ** -8 * exact.abs() + 1.01 * H * 2.0 ** -24 * size
+            assert bool(((h13[lo:hi].double() - exact).abs() <= tol).all())
+    assert some > 10
