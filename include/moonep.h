@@ -547,8 +547,10 @@ int moe_q8_store(int64_t rows, int32_t width, const moe_bf16 *src, uint8_t *q, u
 
 /*
  * dst [rows][width] bf16 = the values that q and scale stand for (exact for
- * what moe_q8_store writes; a code of other origin that passes bf16's range is
- * infinite, one below its last place is cut off).
+ * what moe_q8_store writes, whose scale bytes end at 247; a code of other origin
+ * that passes bf16's range is infinite, one below its last place is cut off).
+ * 2^128, the scale of a byte of 255, is itself infinite: its codes stand for
+ * infinities, codes of zero for NaN.
  */
 int moe_q8_load(int64_t rows, int32_t width, const uint8_t *q, const uint8_t *scale,
                 moe_bf16 *dst, hipStream_t stream);

@@ -1,4 +1,5 @@
-"""Calls on tensors that lie next to each other, and those that may share memory."""
+"""Calls on codes: tensors that lie next to each other or may share memory, scales that no store
+writes, and the same call again."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +8,7 @@ import moe_expert_load_amd as mx
 import test_gpu_q8 as Q
 import workloads as W
 from gpu_helpers import bits, cfgs, free, gpu_plan
+from oracle import bf16, q8
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +163,28 @@ def test_projection_repeats_and_rounds_once(shape):
             tol = 2.0 ** -8 * exact.abs() + 1.01 * H * 2.0 ** -24 * size
             assert bool(((h13[lo:hi].double() - exact).abs() <= tol).all())
     assert some > 10
+
+
+def test_scales_that_no_store_writes():
+    """Scale bytes 248 to 255 under every code: 2^121 to 2^127, and an infinite scale."""
+    q = np.repeat(np.arange(256, dtype=np.uint8)[None], 8, axis=0)
+    s = np.repeat(np.arange(248, 256, dtype=np.uint8)[:, None], 8, axis=1)
+    out = torch.empty((8, 256), dtype=torch.bfloat16, device="cuda")
+    mx.moe_q8_load(8, 256, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), out)
+    torch.cuda.synchronize()
+    got, want = bf16.bits_to_f64(bits(out)), q8.load(q, s)
+    want[7] = np.where(want[7] == 0, np.nan, np.copysign(np.inf, want[7]))       # byte 255
+    want[7, [127, 255]] = np.nan                            # NaN under any scale
+    want[want >= 2.0 ** 128] = np.inf
+    want[want <= -2.0 ** 128] = -np.inf
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_largest_scale_of_a_store():
+    """The largest finite bf16 magnitude: scale byte 247."""
+    b = np.full((1, 32), 0x7F7F, np.uint16)
+    b[0, 1::2] = 0xFF7F
+    q, s = Q.store(b)
+    wq, ws = q8.store(b)
+    assert ws.max() == 247
+    assert np.array_equal(s.cpu().numpy(), ws.reshape(-1)) and np.array_equal(q.cpu().numpy(), wq.reshape(-1))
