@@ -184,9 +184,10 @@ __global__ __launch_bounds__(kQ8Threads) void k_swiglu_bwd_q8(const q8_u32x2* __
 // flight before the first is used; each wave sums its part of their KB dots,
 // and the four waves' parts are added in LDS, pass after pass.  Bound by the
 // scattered rows: 524,288 of 2,048 values in 0.70 ms, 5.0 TB/s (4 routes in
-// flight: 0.71, 2: 0.76), of 7,168 in 2.57 ms, 4.8 TB/s.  One wave takes rows of up to 128 vectors, whose
-// workgroups have too few loads in flight: 262,144 of 512 values in 81 us, 1,024
-// in 189, against 220 and 232 with four waves; of 2,048 both take 0.70 ms.
+// flight: 0.71, 2: 0.76), of 7,168 in 2.57 ms, 4.8 TB/s.  One wave takes rows of
+// up to 128 vectors, whose workgroups have too few loads in flight: 262,144 of 512
+// values in 81 us, 1,024 in 189, against 220 and 232 with four waves; of 2,048 both
+// take 0.70 ms.
 template <int W, int CU, int KB>
 __global__ __launch_bounds__(256) void k_combine_bwd_q8(const u32x4* __restrict__ dout,
                                                         const q8_u32x2* __restrict__ yq,
