@@ -47,6 +47,16 @@
  *                                  the activation again
  *   moe_combine_backward_q8        gradients of combine from y's codes
  *
+ * and products with an epilogue, for experts with biases, shared experts and
+ * the router's own projection, with dropout:
+ *
+ *   moe_grouped_gemm_epilogue  bias, activation, dropout and residual on the
+ *                              way out of a grouped or a single product
+ *   moe_epilogue_backward      gradient of that epilogue, and of the biases
+ *   moe_dropout                dropout and residual; its own backward
+ *   moe_combine_dropout        combine with dropout and residual
+ *   moe_combine_dropout_backward  gradients of that
+ *
  * Prefetch pool ("Moonshot AI 开源 MoonEP", 核心思想: the prefetch slots come
  * from one rank-global pool shared by all layers, so the extra memory is B
  * expert weights per projection in total, not per layer).  w_pref and
@@ -600,6 +610,141 @@ int moe_swiglu_backward_q8(const moe_cfg *cfg, const uint8_t *h13q, const uint8_
 int moe_combine_backward_q8(const moe_cfg *cfg, const moe_plan *plan, const moe_bf16 *dout,
                             const uint8_t *yq, const uint8_t *yscale, const float *gates,
                             moe_bf16 *dy, float *dgates, hipStream_t stream);
+
+/* Activations of the epilogue. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,      /* max(z, 0)                                         */
+  MOE_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution             */
+  MOE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2   */
+  MOE_ACT_SILU = 4,      /* z / (1 + e^-z)                                    */
+  MOE_ACT_RELU2 = 5      /* max(z, 0)^2                                       */
+};
+
+/*
+ * Dropout, wherever it occurs below.  A probability p in [0, 1] is taken in
+ * steps of 2^-16: with d = floor(65536 p + 1/2), a value whose number is below
+ * d becomes 0 and any other is multiplied by 65536 / (65536 - d) (all become 0
+ * at d = 65536; d = 0 changes nothing and reads no rng).  The number of the
+ * value at flat index i of a tensor is 16 bits of a Philox4x32-10 block (Salmon
+ * et al., "Parallel random numbers: as easy as 1, 2, 3", 2011): counter words
+ * (low and high half of floor(i / 8), low and high half of rng[1]), key words
+ * (low and high half of rng[0]); value i % 8 = 2w or 2w + 1 takes the low or
+ * high half of word w.  rng [2] int64 on the device: the seed, and a number that
+ * the caller changes from use to use (the step, say), so a captured graph draws
+ * new numbers when the caller writes new ones there.  A backward given the same
+ * rng contents and the same p drops the same values; no mask is stored.
+ */
+
+/* Settings of an epilogue: a known act, p in [0, 1], f32 0 or 1. */
+typedef struct {
+  int32_t act;  /* MOE_ACT_*                                                  */
+  float p;      /* dropout                                                    */
+  int32_t f32;  /* y, residual and dy are fp32 (1) or bf16 (0)                */
+} moe_epilogue_cfg;
+
+/*
+ * Host only.  Bytes of the `workspace` of moe_grouped_gemm_epilogue and
+ * moe_epilogue_backward.
+ */
+int moe_epilogue_workspace_size(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
+                                size_t *bytes_out);
+
+/*
+ * moe_grouped_gemm with an epilogue ("Moonshot AI 开源 MoonEP", 核心思想: every
+ * expert projection is one [E+B, H, H'] tensor addressed by row index).  For
+ * the rows of every segment j of ranks [rank_begin, rank_end), with fp32
+ * accumulation:
+ *   z = xperm_seg @ W(r, j) + bias[e]
+ *   y = residual + dropout(act(z))
+ * e is the expert whose weights row j holds: j itself below E, slot_expert of
+ * the prefetch slot otherwise (an id outside [0, E) there has no bias), so
+ * biases need no prefetch.  y [R][S*K][Hp] and residual are bf16 or fp32 (f32);
+ * y is rounded once.  pre [R][S*K][Hp] bf16 receives z rounded, for
+ * moe_epilogue_backward.  bias [E][Hp] fp32, residual and pre may be NULL; rng
+ * only if p drops something; dropout's index i counts values of the whole
+ * [R][S*K][Hp] tensor.  Rows outside the listed ranks are not written.
+ *
+ * plan NULL (R = 1 and E = 1): one matrix for all S*K rows -- a shared expert,
+ * the router's projection to logits (f32), any dense layer.  w_home [H][Hp];
+ * w_pref is not read.  moe_grouped_gemm_dgrad and moe_grouped_gemm_wgrad of the
+ * same configuration are its other gradients.
+ *
+ * Few rows (decoding) go to a kernel that reads the weights once with every
+ * compute unit, in a fixed order of sums: the same call gives the same bits, a
+ * call with other rows beside them need not.  y may be residual (in place);
+ * apart from that the listed ranks' rows of y and pre and the workspace
+ * (moe_epilogue_workspace_size() bytes; concurrent calls need distinct ones)
+ * must not overlap each other or the inputs.
+ */
+int moe_grouped_gemm_epilogue(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
+                              const moe_plan *plan, const moe_bf16 *xperm,
+                              const moe_bf16 *w_home, const moe_bf16 *w_pref,
+                              const float *bias, const void *residual, const int64_t *rng,
+                              void *y, moe_bf16 *pre, int32_t rank_begin, int32_t rank_end,
+                              void *workspace, hipStream_t stream);
+
+/*
+ * Gradients of that epilogue by z and by the biases, over all ranks, from dy
+ * [R][S*K][Hp] (bf16 or fp32) and the kept pre:
+ *   dz       = act'(pre) * (kept ? dy * scale : 0)      rounded once to bf16
+ *   dbias[e] = sum over the rows of e's segments on every rank of the same
+ *              product in fp32 (home, overflow and prefetch rows; zero for an
+ *              expert without rows), in a fixed order
+ * dz [R][S*K][Hp] is dy of moe_grouped_gemm_dgrad and moe_grouped_gemm_wgrad;
+ * every row is written.  dbias [E][Hp] fp32 is complete: moe_reduce_grad is not
+ * for it.  Either may be NULL, not both; pre may be NULL with MOE_ACT_NONE; plan
+ * is read only for dbias and may be NULL without it, or as above.  The
+ * gradient by the residual is dy itself.  At z = 0 the slope of MOE_ACT_RELU is
+ * 0.  dz may be pre, or dy if that is bf16 (in place); apart from that dz, dbias
+ * and the workspace must not overlap each other or the inputs.
+ */
+int moe_epilogue_backward(const moe_cfg *cfg, const moe_epilogue_cfg *ec, const moe_plan *plan,
+                          const void *dy, const moe_bf16 *pre, const int64_t *rng, moe_bf16 *dz,
+                          float *dbias, void *workspace, hipStream_t stream);
+
+/* Settings of dropout: p in [0, 1], f32 0 or 1. */
+typedef struct {
+  float p;
+  int32_t f32;  /* the token rows (src, residual, dst, out, dout) are fp32 (1) or bf16 (0) */
+} moe_dropout_cfg;
+
+/*
+ * dst = residual + dropout(src) for `rows` rows of `width` values, in fp32,
+ * rounded once.  residual may be NULL: dst = dropout(src), which is also the
+ * backward (src the gradient, the same rng).  dst may be src or residual (in
+ * place) and must not overlap them otherwise, nor rng.  width % 8 == 0, width >=
+ * 8, rows >= 0, rows * width < 2^40 (MOE_ELIMIT).
+ */
+int moe_dropout(const moe_dropout_cfg *dc, int64_t rows, int32_t width, const void *src,
+                const void *residual, const int64_t *rng, void *dst, hipStream_t stream);
+
+/*
+ * moe_combine with dropout and the residual stream:
+ *   out[t] = residual[t] + dropout( sum_{k ascending} gates[t][k] * y[route[t*K + k]] )
+ * in fp32, rounded once to out's type.  out and residual [R*S][Hp] are bf16 or
+ * fp32 (f32); residual may be NULL and may be out (in place); rng only if p
+ * drops something, its index i counting values of [R*S][Hp].  out must not
+ * overlap anything else that is read.
+ */
+int moe_combine_dropout(const moe_cfg *cfg, const moe_dropout_cfg *dc, const moe_plan *plan,
+                        const moe_bf16 *y, const float *gates, const void *residual,
+                        const int64_t *rng, void *out, hipStream_t stream);
+
+/*
+ * Gradients of moe_combine_dropout: with d[t] = kept ? dout[t] * scale : 0 (fp32,
+ * dout [R*S][Hp] bf16 or fp32), for every token t and k with q = route[t*K + k]
+ * >= 0:
+ *   dy[q]        = bf16( gates[t][k] * d[t] )
+ *   dgates[t][k] = sum_h d[t][h] * y[q][h]      (fp32)
+ * dgates[t][k] = 0 for routes of -1.  Rows of dy no route names are not
+ * written.  The gradient by the residual is dout itself.  dgates may be gates
+ * (in place); dy and dgates must not overlap the inputs or each other otherwise.
+ */
+int moe_combine_dropout_backward(const moe_cfg *cfg, const moe_dropout_cfg *dc,
+                                 const moe_plan *plan, const void *dout, const moe_bf16 *y,
+                                 const float *gates, const int64_t *rng, moe_bf16 *dy,
+                                 float *dgates, hipStream_t stream);
 
 /* Host only.  Static text for a MOE_* return code. */
 const char *moe_strerror(int code);

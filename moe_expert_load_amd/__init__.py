@@ -18,6 +18,7 @@ MODE_TRAIN, MODE_INFER = 0, 1
 STATUS_BAD_ID, STATUS_UNBALANCED, STATUS_CAPACITY, STATUS_INTERNAL = 1, 2, 4, 8
 PLAN_ASCENDING, PLAN_LARGEST_FIRST = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_RELU2 = range(6)
 PLAN_FIELDS = ("counts", "load0", "route", "cu_seqlens", "slot_expert",
                "n_redundant", "src_rank", "moves", "status", "workspace")
 ENTRY_POINTS = ("moe_plan_sizes", "moe_plan_run", "moe_plan_run_policy", "moe_prefetch_weight",
@@ -30,7 +31,9 @@ ENTRY_POINTS = ("moe_plan_sizes", "moe_plan_run", "moe_plan_run_policy", "moe_pr
                 "moe_router_workspace_size", "moe_router", "moe_balance_loss",
                 "moe_router_backward", "moe_q8_store", "moe_q8_load", "moe_dispatch_q8",
                 "moe_grouped_gemm_swiglu_q8", "moe_swiglu_backward_q8",
-                "moe_combine_backward_q8", "moe_strerror")
+                "moe_combine_backward_q8", "moe_epilogue_workspace_size",
+                "moe_grouped_gemm_epilogue", "moe_epilogue_backward", "moe_dropout",
+                "moe_combine_dropout", "moe_combine_dropout_backward", "moe_strerror")
 
 
 class MoeError(RuntimeError):
@@ -50,6 +53,14 @@ class moe_router_cfg(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("logits_bf16", ctypes.c_int32),
                 ("nseq", ctypes.c_int32)]
+
+
+class moe_epilogue_cfg(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("p", ctypes.c_float), ("f32", ctypes.c_int32)]
+
+
+class moe_dropout_cfg(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("f32", ctypes.c_int32)]
 
 
 class moe_plan(ctypes.Structure):
@@ -73,6 +84,8 @@ def load(path=None):
     C = ctypes.POINTER(moe_cfg)
     PL = ctypes.POINTER(moe_plan)
     RC = ctypes.POINTER(moe_router_cfg)
+    EC = ctypes.POINTER(moe_epilogue_cfg)
+    DC = ctypes.POINTER(moe_dropout_cfg)
     sig = {
         "moe_plan_sizes": [C, ctypes.POINTER(SZ)],
         "moe_plan_run": [C, P, PL, P],
@@ -102,6 +115,12 @@ def load(path=None):
         "moe_grouped_gemm_swiglu_q8": [C, P, P, P, P, P, P, P, I32, I32, P, P],
         "moe_swiglu_backward_q8": [C, P, P, P, P, P, P],
         "moe_combine_backward_q8": [C, PL, P, P, P, P, P, P, P],
+        "moe_epilogue_workspace_size": [C, EC, ctypes.POINTER(SZ)],
+        "moe_grouped_gemm_epilogue": [C, EC, PL, P, P, P, P, P, P, P, P, I32, I32, P, P],
+        "moe_epilogue_backward": [C, EC, PL, P, P, P, P, P, P, P],
+        "moe_dropout": [DC, I64, I32, P, P, P, P, P],
+        "moe_combine_dropout": [C, DC, PL, P, P, P, P, P, P],
+        "moe_combine_dropout_backward": [C, DC, PL, P, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -536,3 +555,110 @@ def moe_combine_backward_q8(cfg, plan, dout, yq, yscale, gates, dy, dgates, stre
         _arg(dy, torch.bfloat16, rows * cfg.Hp, "dy", dev),
         _arg(dgates, torch.float32, rows, "dgates", dev), _on(stream, dev)),
         "moe_combine_backward_q8")
+
+
+def make_epilogue_cfg(act=ACT_NONE, p=0.0, f32=False):
+    return moe_epilogue_cfg(int(act), float(p), int(f32))
+
+
+def make_dropout_cfg(p=0.0, f32=False):
+    return moe_dropout_cfg(float(p), int(f32))
+
+
+def moe_epilogue_workspace_size(cfg, ecfg):
+    out = ctypes.c_size_t()
+    _check(load().moe_epilogue_workspace_size(ctypes.byref(cfg), ctypes.byref(ecfg),
+                                              ctypes.byref(out)), "moe_epilogue_workspace_size")
+    return int(out.value)
+
+
+def _row_type(f32):
+    return torch.float32 if f32 else torch.bfloat16
+
+
+def _rng(rng, dev):
+    """Seed and step of dropout: two int64 on the device."""
+    return _arg(rng, torch.int64, 2, "rng", dev)
+
+
+def _plan_or_none(cfg, plan, dev):
+    if plan is None:
+        return None
+    _arg(plan.cu_seqlens, torch.int32, cfg.R * (cfg.E + cfg.B + 1), "plan", dev)
+    return plan.c
+
+
+def moe_grouped_gemm_epilogue(cfg, ecfg, plan, xperm, w_home, w_pref, bias, residual, rng, y,
+                              pre, rank_begin, rank_end, workspace, stream=None):
+    """plan None: one matrix for all rows (cfg.R = cfg.E = 1); w_pref is then not read."""
+    dev = torch.cuda.current_device()
+    rows = cfg.R * cfg.S * cfg.K
+    hh = cfg.H * cfg.Hp
+    bf, out = torch.bfloat16, _row_type(ecfg.f32)
+    slots = plan is not None and cfg.B
+    _check(load().moe_grouped_gemm_epilogue(
+        ctypes.byref(cfg), ctypes.byref(ecfg), _plan_or_none(cfg, plan, dev),
+        _arg(xperm, bf, rows * cfg.H, "xperm", dev),
+        _arg(w_home, bf, cfg.E * hh, "w_home", dev),
+        _arg(w_pref, bf, cfg.R * cfg.B * hh, "w_pref", dev) if slots else None,
+        _arg(bias, torch.float32, cfg.E * cfg.Hp, "bias", dev),
+        _arg(residual, out, rows * cfg.Hp, "residual", dev), _rng(rng, dev),
+        _arg(y, out, rows * cfg.Hp, "y", dev), _arg(pre, bf, rows * cfg.Hp, "pre", dev),
+        int(rank_begin), int(rank_end),
+        _arg(workspace, torch.uint8, moe_epilogue_workspace_size(cfg, ecfg), "workspace", dev),
+        _on(stream, dev)), "moe_grouped_gemm_epilogue")
+
+
+def moe_epilogue_backward(cfg, ecfg, plan, dy, pre, rng, dz, dbias, workspace=None, stream=None):
+    """dz or dbias may be None; plan and workspace are needed for dbias only."""
+    dev = torch.cuda.current_device()
+    rows = cfg.R * cfg.S * cfg.K
+    bf = torch.bfloat16
+    need = moe_epilogue_workspace_size(cfg, ecfg) if dbias is not None else 0
+    _check(load().moe_epilogue_backward(
+        ctypes.byref(cfg), ctypes.byref(ecfg), _plan_or_none(cfg, plan, dev),
+        _arg(dy, _row_type(ecfg.f32), rows * cfg.Hp, "dy", dev),
+        _arg(pre, bf, rows * cfg.Hp, "pre", dev), _rng(rng, dev),
+        _arg(dz, bf, rows * cfg.Hp, "dz", dev),
+        _arg(dbias, torch.float32, cfg.E * cfg.Hp, "dbias", dev),
+        _arg(workspace, torch.uint8, need, "workspace", dev), _on(stream, dev)),
+        "moe_epilogue_backward")
+
+
+def moe_dropout(dcfg, rows, width, src, residual, rng, dst, stream=None):
+    """dst = residual + dropout(src); residual may be None."""
+    dev = torch.cuda.current_device()
+    n, to = rows * width, _row_type(dcfg.f32)
+    _check(load().moe_dropout(
+        ctypes.byref(dcfg), rows, width, _arg(src, to, n, "src", dev),
+        _arg(residual, to, n, "residual", dev), _rng(rng, dev), _arg(dst, to, n, "dst", dev),
+        _on(stream, dev)), "moe_dropout")
+
+
+def moe_combine_dropout(cfg, dcfg, plan, y, gates, residual, rng, out, stream=None):
+    """residual may be None, rng with p = 0."""
+    dev = torch.cuda.current_device()
+    ntok = cfg.R * cfg.S
+    to = _row_type(dcfg.f32)
+    _arg(plan.route, torch.int32, ntok * cfg.K, "plan", dev)
+    _check(load().moe_combine_dropout(
+        ctypes.byref(cfg), ctypes.byref(dcfg), plan.c,
+        _arg(y, torch.bfloat16, ntok * cfg.K * cfg.Hp, "y", dev),
+        _arg(gates, torch.float32, ntok * cfg.K, "gates", dev),
+        _arg(residual, to, ntok * cfg.Hp, "residual", dev), _rng(rng, dev),
+        _arg(out, to, ntok * cfg.Hp, "out", dev), _on(stream, dev)), "moe_combine_dropout")
+
+
+def moe_combine_dropout_backward(cfg, dcfg, plan, dout, y, gates, rng, dy, dgates, stream=None):
+    dev = torch.cuda.current_device()
+    ntok = cfg.R * cfg.S
+    rows = ntok * cfg.K
+    bf = torch.bfloat16
+    _arg(plan.route, torch.int32, rows, "plan", dev)
+    _check(load().moe_combine_dropout_backward(
+        ctypes.byref(cfg), ctypes.byref(dcfg), plan.c,
+        _arg(dout, _row_type(dcfg.f32), ntok * cfg.Hp, "dout", dev),
+        _arg(y, bf, rows * cfg.Hp, "y", dev), _arg(gates, torch.float32, rows, "gates", dev),
+        _rng(rng, dev), _arg(dy, bf, rows * cfg.Hp, "dy", dev),
+        _arg(dgates, torch.float32, rows, "dgates", dev), _on(stream, dev)),
+        "moe_combine_dropout_backward")
