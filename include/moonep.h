@@ -675,7 +675,8 @@ int moe_epilogue_workspace_size(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
  * call with other rows beside them need not.  y may be residual (in place);
  * apart from that the listed ranks' rows of y and pre and the workspace
  * (moe_epilogue_workspace_size() bytes; concurrent calls need distinct ones)
- * must not overlap each other or the inputs.
+ * must not overlap each other or the inputs.  MOE_ELIMIT from 2^24 tiles of 128
+ * rows and 256 columns on (every segment's last tile counted whole).
  */
 int moe_grouped_gemm_epilogue(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
                               const moe_plan *plan, const moe_bf16 *xperm,

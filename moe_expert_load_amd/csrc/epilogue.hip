@@ -12,7 +12,6 @@
 #include <algorithm>
 
 #include "epilogue.hpp"
-#include "few.hpp"
 #include "host.hpp"
 #include "overlap.hpp"
 

@@ -182,32 +182,103 @@ struct Epilogue {
   float scale;
 };
 
-// Columns n .. n + 7 of row `row` from their products z and biases b.
-__device__ __forceinline__ void epilogue8(const Epilogue& ep, const DropKey& key, float (&z)[8],
-                                          const float (&b)[8], int64_t row, int n) {
-  const int64_t at = row * ep.N + n;
+// Eight residual values as they lie in memory (bf16: the first half only).
+struct Residual8 {
+  u32x4 v[2];
+};
+__device__ __forceinline__ Residual8 residual8(const Epilogue& ep, int64_t at) {
+  Residual8 r;
+  if (ep.f32) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(ep.residual) + at);
+    r.v[0] = p[0];
+    r.v[1] = p[1];
+  } else {
+    r.v[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(ep.residual) + at);
+    r.v[1] = u32x4{0, 0, 0, 0};
+  }
+  return r;
+}
+
+// z + residual, rounded once, to y.
+__device__ __forceinline__ void finish8(const Epilogue& ep, float (&z)[8], const Residual8& r,
+                                        int64_t at) {
+  if (ep.f32) {
+    if (ep.residual)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] += b[i];
+      for (int i = 0; i < 8; ++i) z[i] += __uint_as_float(r.v[i >> 2][i & 3]);
+    store8(static_cast<float*>(ep.y) + at, z);
+  } else {
+    if (ep.residual)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[2 * q] += bf16_lo(r.v[0][q]);
+        z[2 * q + 1] += bf16_hi(r.v[0][q]);
+      }
+    store8(static_cast<uint16_t*>(ep.y) + at, z);
+  }
+}
+
+// pre, activation and dropout of z = product + bias.
+__device__ __forceinline__ void middle8(const Epilogue& ep, const DropKey& key, float (&z)[8],
+                                        int64_t at) {
   if (ep.pre) store8(ep.pre + at, z);
   act8(z, ep.act);
   if (ep.cut) drop8(z, key, uint64_t(at) >> 3, ep.cut, ep.scale);
-  if (ep.f32) {
-    if (ep.residual) {
-      float r[8];
-      load8(static_cast<const float*>(ep.residual) + at, r);
+}
+
+// Columns n .. n + 7 of row `row` from their products z and biases b.  The
+// residual is asked for first: the rest covers its latency.
+__device__ __forceinline__ void epilogue8(const Epilogue& ep, const DropKey& key, float (&z)[8],
+                                          const float (&b)[8], int64_t row, int n) {
+  const int64_t at = row * ep.N + n;
+  Residual8 r{};
+  if (ep.residual) r = residual8(ep, at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += r[i];
-    }
-    store8(static_cast<float*>(ep.y) + at, z);
-  } else {
-    if (ep.residual) {
-      float r[8];
-      load8(static_cast<const uint16_t*>(ep.residual) + at, r);
+  for (int i = 0; i < 8; ++i) z[i] += b[i];
+  middle8(ep, key, z, at);
+  finish8(ep, z, r, at);
+}
+
+// A wave's block of z staged in LDS: groups 0 .. 7 of this lane, group k at
+// place(k, at) (its eight values; `at` the flat index of the first in y), null
+// where there is none.  All residuals are asked for before the first group's
+// arithmetic, which is a loop of its own (the activations are long code) and
+// leaves its values where they were; the last loop only adds and stores.
+template <typename Place>
+__device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey& key,
+                                               Place&& place) {
+  Residual8 r[8];
+  if (ep.residual)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += r[i];
+    for (int k = 0; k < 8; ++k) {
+      int64_t at = 0;
+      if (place(k, at)) r[k] = residual8(ep, at);
     }
-    store8(static_cast<uint16_t*>(ep.y) + at, z);
+  if (ep.pre || ep.cut || ep.act != MOE_ACT_NONE)
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      int64_t at = 0;
+      float* p = place(k, at);
+      if (!p) continue;
+      float z[8];
+      load8(p, z);
+      middle8(ep, key, z, at);
+      store8(p, z);
+    }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    int64_t at = 0;
+    float* p = place(k, at);
+    if (!p) continue;
+    float z[8];
+    load8(p, z);
+    finish8(ep, z, r[k], at);
   }
+}
+
+// Bias of column n of expert e, 0 without one.
+__device__ __forceinline__ float bias1(const Epilogue& ep, int e, int E, int n) {
+  return ep.bias && (unsigned)e < (unsigned)E && n < ep.N ? ep.bias[int64_t(e) * ep.N + n] : 0.f;
 }
 
 // Biases of columns n .. n + 7 of expert e; an id outside [0, E) has none.
@@ -242,6 +313,9 @@ inline bool valid_epilogue(const moe_epilogue_cfg* ec) {
   return ec && ec->act >= MOE_ACT_NONE && ec->act <= MOE_ACT_RELU2 &&
          (ec->f32 == 0 || ec->f32 == 1) && drop_params(ec->p, &cut, &scale);
 }
+
+// Bytes of workspace of the epilogue's backward (epilogue.hip).
+size_t epilogue_bwd_ws_bytes(const moe_cfg* c);
 
 // The shape that a null plan stands for: every row belongs to one matrix.
 inline bool one_matrix(const moe_cfg* c) { return c->R == 1 && c->E == 1; }

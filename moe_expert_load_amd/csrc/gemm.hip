@@ -30,8 +30,7 @@
 //   gate and the same 128 up columns, interleaved in 32-column blocks, so
 //   every wave holds gate and up of the same outputs in its accumulators
 //   and applies the activation in registers; MODE 4: the same, with gate
-//   and up kept as 8-bit codes (q8.hpp) instead of bf16; MODE 5: the forward
-//   with bias, activation, dropout and residual (epilogue.hpp) on its way out.
+//   and up kept as 8-bit codes (q8.hpp) instead of bf16.
 // Tile: BM = BN = 256, BK = 32; 4 waves in a 2x2 grid, each 128x128 =
 // 4x4 MFMA blocks of 32x32 with fp32 accumulators (256 AGPRs per wave).
 // Operands go from global memory straight into LDS (buffer_load ... lds,
@@ -53,20 +52,12 @@
 #include <type_traits>
 
 #include "common.hpp"
-#include "epilogue.hpp"
-#include "few.hpp"
 #include "host.hpp"
+#include "lds.hpp"
 #include "overlap.hpp"
 #include "q8.hpp"
 
 namespace moonep {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short i16x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr int BM = 256, BN = 256;
 
@@ -90,9 +81,7 @@ constexpr int kABlock = 64;     // rows between a wave's row blocks
 #endif
 constexpr int kBand = MOONEP_GEMM_BAND;
 
-enum {
-  MODE_FWD = 0, MODE_WGRAD = 1, MODE_DGRAD = 2, MODE_SWIGLU = 3, MODE_SWIGLU_Q8 = 4, MODE_EPI = 5
-};
+enum { MODE_FWD = 0, MODE_WGRAD = 1, MODE_DGRAD = 2, MODE_SWIGLU = 3, MODE_SWIGLU_Q8 = 4 };
 
 struct WorkItem {
   int32_t r, j, row0, rows;  // rank, weight row, first xperm row (absolute), row count
@@ -114,59 +103,10 @@ struct GemmArgs {
   int32_t H, Hp, E, B, SK;
   uint8_t* h13q;              // MODE_SWIGLU_Q8: codes and scale bytes of gate and up
   uint8_t* h13s;
-  Epilogue ep;                // MODE_EPI
 };
 
 // Cache-policy operand of the buffer-store builtin: non-temporal.
 constexpr int kStoreNT = 2;
-
-// Range-checked buffer resource over [base, base + bytes): loads past the end
-// return zeros (per dword), which pads ragged row/K tails with zeros.
-__device__ __forceinline__ u32x4 make_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  return u32x4{uint32_t(b), uint32_t(b >> 32) & 0xffffu, bytes, 0x00020000u};
-}
-
-// 16 bytes per lane from global memory straight into LDS (buffer_load ...
-// lds): lane l writes lds_dst + 16*l; lds_dst must be wave-uniform.  Issued
-// as inline assembly so the compiler does not pair every later LDS read with
-// a wait for all such loads; the kernel waits for each stage itself
-// (wait_vm) before the barrier that publishes it.
-__device__ __forceinline__ void load_lds16(u32x4 rsrc, const unsigned char* lds_dst,
-                                           uint32_t voff, uint32_t soff) {
-  // every operand but voff is wave-uniform; make that explicit (scalar regs)
-  const uint32_t l =
-      (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)lds_dst);
-  u32x4 r;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) r[q] = (uint32_t)__builtin_amdgcn_readfirstlane((int)rsrc[q]);
-  const uint32_t so = (uint32_t)__builtin_amdgcn_readfirstlane((int)soff);
-  // one wait state between the scalar write of M0 and the LDS-DMA load that
-  // reads it (a hazard of this GPU generation that the compiler's hazard pass
-  // cannot see inside inline assembly)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(l), "v"(voff), "s"(r), "s"(so) : "memory");
-}
-
-// Wait until at most N vector-memory operations of this wave are in flight.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N < 64, "vmcnt");
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-
-// Transposing LDS read: the 16 lanes of a group each name a 64-bit piece
-// (4 bf16) of a 4-row x 16-column block; lane (a, c) = (i/4, i%4) receives
-// column 4a + c of rows 0..3.  Used so that an operand stored [k][col] in
-// LDS arrives as 8 consecutive k per lane, the MFMA layout.
-__device__ __forceinline__ u32x2 lds_tr(const unsigned char* p) {
-  const i16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-  return __builtin_bit_cast(u32x2, v);
-}
-
-__device__ __forceinline__ bf16x8 join(u32x2 lo, u32x2 hi) {
-  return __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-}
 
 // Pipeline: kNST stages of BK-deep k-tiles.  BK = 64 (2 stages of 64 KB)
 // makes every row of the k-contiguous forward operand a whole 128-byte line
@@ -269,11 +209,6 @@ __device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// Workgroup barrier that orders this wave's LDS accesses around it but does
-// not wait for outstanding global loads (the direct-to-LDS loads of later
-// stages stay in flight; each wave waits for its own with wait_vm first).
-__device__ __forceinline__ void barrier_lds() { asm volatile("s_barrier" ::: "memory"); }
-
 // Tiles of one pipeline stage:
 //  * "row tile" [256 rows][BK k] (forward A, k contiguous): 16-byte chunk kc
 //    of row m is stored at chunk kc ^ ((m >> RSH) & (CPR - 1)) (CPR = BK/8
@@ -316,11 +251,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
   // projection).
   constexpr bool kQ8 = MODE == MODE_SWIGLU_Q8;
   constexpr bool kSwi = MODE == MODE_SWIGLU || kQ8;
-  constexpr bool kEpi = MODE == MODE_EPI;
-  constexpr bool kPair = (MODE == MODE_FWD || MODE == MODE_DGRAD || kSwi || kEpi) &&
+  constexpr bool kPair = (MODE == MODE_FWD || MODE == MODE_DGRAD || kSwi) &&
                          MOONEP_GEMM_PAIRA && BK == 32 && kNST == 4;
   constexpr bool kNMajor =
-      MODE == MODE_DGRAD || ((MODE == MODE_FWD || kSwi || kEpi) && MOONEP_FWD_NMAJOR);
+      MODE == MODE_DGRAD || ((MODE == MODE_FWD || kSwi) && MOONEP_FWD_NMAJOR);
   const int H = g.H, Hp = g.Hp;
   const int WC = kSwi ? 2 * Hp : Hp;                     // weight / dy row length
   const int NOUT = MODE == MODE_DGRAD ? H : Hp;          // output columns
@@ -928,52 +862,6 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       }
       __syncthreads();
-    } else if constexpr (kEpi) {
-      // Per wave, four passes of 32 rows x 128 columns staged in fp32 in its
-      // own 16 KB (512-byte rows; the two lane halves, 4 rows apart, swap the
-      // halves of a row's 64-column group so that they write different banks),
-      // so that a lane gets eight consecutive columns of a row: one group of
-      // dropout's numbers and one 16-byte store.  A lane's columns are the same
-      // in every pass; their biases stay in registers.
-      unsigned char* Cs = kPair ? (wv < 2 ? g_pa0 : g_pa1) + (wv & 1) * 16384 : epilogue_area(wv);
-      const int n = n0 + wn * 128 + (lane & 15) * 8;
-      float b[8];
-      bias8(g.ep, expert_of(g.ep, it.r, it.j, g.E, g.B), g.E, n, b);
-      DropKey key{};
-      if (g.ep.cut) key = drop_key(g.ep.rng);
-      unsigned char* cbase = Cs + 4 * (lane >> 5) * 512 + (lane & 31) * 4;
-      const int half = lane >> 5;
-      // a loop, not four copies: the activations are long
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        if (64 * i + wm * kAWaveRow >= it.rows) break;         // uniform: no row is left
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x16 a = i == 0 ? acc[0][j] : i == 1 ? acc[1][j] : i == 2 ? acc[2][j] : acc[3][j];
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            *reinterpret_cast<float*>(cbase + (8 * (v >> 2) + (v & 3)) * 512 + ((j ^ half) * 128)) =
-                a[v];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          const int rr = 4 * k + (lane >> 4);
-          // rows 4 .. 7 of every eight were written by the upper lane half
-          const int c4 = ((lane & 15) >> 2) ^ ((rr >> 2) & 1);
-          float z[8];
-          load8(reinterpret_cast<const float*>(Cs + rr * 512 + c4 * 128 + (lane & 3) * 32), z);
-          const int m = 64 * i + wm * kAWaveRow + rr;
-          if (m < it.rows && n < NOUT) epilogue8(g.ep, key, z, b, int64_t(it.row0) + m, n);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      }
-      __syncthreads();
     } else {
       // Per wave, two passes of 64 rows x 128 columns staged as bf16 in the
       // wave's own 16 KB stage array (256-byte rows; pairs of rows converted
@@ -1553,12 +1441,6 @@ static size_t gemm_ws_bytes(const moe_cfg* c) {
   return std::max(fwd_ws_bytes(c, c->R), 256 + size_t(wgrad_capacity(c)) * sizeof(WorkItem));
 }
 
-// One workspace for the product with an epilogue by either kernel and for the
-// epilogue's backward.
-static size_t epilogue_ws_bytes(const moe_cfg* c) {
-  return std::max({fwd_ws_bytes(c, c->R), few_ws_bytes(c), epilogue_bwd_ws_bytes(c)});
-}
-
 // Cost model of the forward-type schedules, picoseconds: a 256x256 tile of
 // class c (2c of 8 MFMA row blocks) over nk 32-deep k-tiles takes
 // tile + nk (k + k_block c); a persistent launch adds `launch`.  Fitted by
@@ -1637,7 +1519,6 @@ static int launch_gemm(int mode, const moe_cfg* c, GemmArgs& g, SchedArgs& s, hi
   if (mode == MODE_FWD) launch_classes<MODE_FWD>(g, s, G, stream);
   else if (mode == MODE_SWIGLU) launch_classes<MODE_SWIGLU>(g, s, G, stream);
   else if (mode == MODE_SWIGLU_Q8) launch_classes<MODE_SWIGLU_Q8>(g, s, G, stream);
-  else if (mode == MODE_EPI) launch_classes<MODE_EPI>(g, s, G, stream);
   else launch_classes<MODE_DGRAD>(g, s, G, stream);
   return hip_status();
 }
@@ -1790,91 +1671,6 @@ extern "C" int moe_grouped_gemm_swiglu_q8(const moe_cfg* cfg, const moe_bf16* xp
                                           int32_t rank_end, void* workspace, hipStream_t stream) {
   return swiglu_projection(cfg, xperm, w13_home, w13_pref, cu_seqlens, act, nullptr, h13q,
                            h13scale, true, rank_begin, rank_end, workspace, stream);
-}
-
-// The work list of one matrix: its row tiles in order.
-namespace moonep {
-__global__ __launch_bounds__(256) void k_one_matrix(WorkItem* items, int32_t* hdr, int rows,
-                                                    int cnt) {
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < cnt; i += gridDim.x * 256)
-    items[i] = WorkItem{0, 0, i * BM, min(BM, rows - i * BM), 0, cnt};
-  if (blockIdx.x == 0 && threadIdx.x == 0) hdr[0] = cnt;
-}
-}  // namespace moonep
-
-extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_cfg* ec,
-                                         const moe_plan* plan, const moe_bf16* xperm,
-                                         const moe_bf16* w_home, const moe_bf16* w_pref,
-                                         const float* bias, const void* residual,
-                                         const int64_t* rng, void* y, moe_bf16* pre,
-                                         int32_t rank_begin, int32_t rank_end, void* workspace,
-                                         hipStream_t stream) {
-  const int rc = check_cfg(cfg);
-  if (rc != MOE_OK) return rc;
-  if (!valid_epilogue(ec)) return MOE_EINVAL;
-  if (rank_begin < 0 || rank_end > cfg->R || rank_begin > rank_end) return MOE_EINVAL;
-  if (!plan && !one_matrix(cfg)) return MOE_EINVAL;
-  if (rank_begin == rank_end || cfg->S == 0) return MOE_OK;
-  uint32_t cut = 0;
-  float scale = 1.f;
-  drop_params(ec->p, &cut, &scale);
-  const bool slots = plan && cfg->B > 0;
-  if (!xperm || !w_home || !y || !workspace || (cut && !rng)) return MOE_EINVAL;
-  if (plan && !plan->cu_seqlens) return MOE_EINVAL;
-  if (slots && (!w_pref || !plan->slot_expert)) return MOE_EINVAL;
-  if (!aligned16(xperm, w_home, slots ? w_pref : nullptr, bias, residual, y, pre, workspace))
-    return MOE_EINVAL;
-  // the listed ranks' parts of every tensor
-  const int64_t SK = int64_t(cfg->S) * cfg->K, first = rank_begin * SK;
-  const int64_t nr = rank_end - rank_begin, rows = nr * SK, segs = cfg->E + cfg->B;
-  const int64_t out = cfg->Hp * (ec->f32 ? 4 : 2), w = int64_t(cfg->H) * cfg->Hp * 2;
-  const char* yb = static_cast<const char*>(y) + first * out;
-  const char* rb = residual ? static_cast<const char*>(residual) + first * out : nullptr;
-  if (clash({{yb, rows * out},
-             {pre ? pre + first * cfg->Hp : nullptr, rows * cfg->Hp * 2},
-             {workspace, (int64_t)epilogue_ws_bytes(cfg)}},
-            {{xperm + first * cfg->H, rows * cfg->H * 2},
-             {w_home, cfg->E * w},
-             {slots ? w_pref + int64_t(rank_begin) * cfg->B * (w / 2) : nullptr, nr * cfg->B * w},
-             {plan ? plan->cu_seqlens + rank_begin * (segs + 1) : nullptr, nr * (segs + 1) * 4},
-             {slots ? plan->slot_expert : nullptr, int64_t(cfg->R) * cfg->B * 4},
-             {bias, int64_t(cfg->E) * cfg->Hp * 4},
-             {rb == yb ? nullptr : rb, rows * out},
-             {cut ? rng : nullptr, 16}}) ||
-      overlap(pre ? pre + first * cfg->Hp : nullptr, rows * cfg->Hp * 2, rb, rows * out) ||
-      overlap(workspace, (int64_t)epilogue_ws_bytes(cfg), rb, rows * out))
-    return MOE_EINVAL;
-  Epilogue ep{};
-  ep.bias = bias; ep.residual = residual; ep.rng = cut ? rng : nullptr; ep.y = y; ep.pre = pre;
-  ep.slot_expert = slots ? plan->slot_expert : nullptr;
-  ep.act = ec->act; ep.f32 = ec->f32; ep.N = cfg->Hp; ep.cut = cut; ep.scale = scale;
-  const int32_t* cu = plan ? plan->cu_seqlens : nullptr;
-  const int cus = num_cus();
-  if (few_rows(cfg, !plan, nr, cus))
-    return launch_few(cfg, xperm, w_home, w_pref, cu, ep, rank_begin, rank_end, workspace, stream);
-  GemmArgs g{};
-  g.xperm = xperm; g.w_home = w_home; g.w_pref = w_pref;
-  g.H = cfg->H; g.Hp = cfg->Hp; g.E = cfg->E; g.B = cfg->B; g.SK = cfg->S * cfg->K;
-  g.ep = ep;
-  SchedArgs s = fwd_sched_args(cfg, cu, workspace, rank_begin, rank_end);
-  if (plan) return launch_gemm(MODE_EPI, cfg, g, s, stream);
-  const int cnt = (cfg->S + BM - 1) / BM;
-  hipLaunchKernelGGL(k_one_matrix, dim3(std::min(256, (cnt + 255) / 256)), dim3(256), 0, stream,
-                     s.items, s.hdr, cfg->S, cnt);
-  g.items = s.items;
-  g.nitems = s.hdr;
-  const int G = std::max(8, cus - cus % 8);
-  hipLaunchKernelGGL((k_gemm<MODE_EPI, 4>), dim3(G), dim3(kGemmThreads), 0, stream, g);
-  return hip_status();
-}
-
-extern "C" int moe_epilogue_workspace_size(const moe_cfg* cfg, const moe_epilogue_cfg* ec,
-                                           size_t* bytes_out) {
-  const int rc = check_cfg(cfg);
-  if (rc != MOE_OK) return rc;
-  if (!valid_epilogue(ec) || !bytes_out) return MOE_EINVAL;
-  *bytes_out = epilogue_ws_bytes(cfg);
-  return MOE_OK;
 }
 
 extern "C" int moe_grouped_gemm_dgrad(const moe_cfg* cfg, const moe_bf16* dy, const moe_bf16* w_home,

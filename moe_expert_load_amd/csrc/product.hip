@@ -1,0 +1,831 @@
+// Products of rows with one matrix or with one per expert, and the epilogue
+// (epilogue.hpp), in four kernels by the height of their tiles; the time of each
+// is modelled on the host (kTiles) and the shortest taken.  The grid covers the
+// tiles that a configuration can have; which there are is listed on the device
+// from cu_seqlens (k_row_blocks).  Where the tiles would leave units idle the k
+// axis is cut into parts whose sums go to the workspace in fp32; k_join adds them
+// in a fixed order and applies the epilogue.
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "epilogue.hpp"
+
+#include "host.hpp"
+#include "lds.hpp"
+#include "overlap.hpp"
+
+namespace moonep {
+
+constexpr int kFewCols = 128;        // columns of a wave
+constexpr int kFewStep = 32;         // k of a step
+constexpr int kBand = 8;             // row blocks of a band, about
+
+struct RowItem {
+  int32_t r, j, row0, rows;  // rank, weight row, first row (absolute), rows
+  int32_t first, cnt;        // its segment's first item, and how many there are
+};
+
+struct ProductArgs {
+  const uint16_t* x;
+  const uint16_t* w_home;
+  const uint16_t* w_pref;
+  const int32_t* cu;         // null: one matrix
+  float* partial;            // [splits][rows][N]
+  int32_t* nblocks;          // grouped: how many of `list` there are
+  int32_t* row_expert;       // [rows], grouped
+  RowItem* list;             // grouped
+  int32_t H, E, B, SK, first_rank, nranks;
+  int32_t rows, height, cols, strips, steps, splits;
+  int32_t blocks;            // grouped: the most there may be
+  Epilogue ep;
+};
+
+// The listed ranks' segments as blocks of at most a.height rows, in layout
+// order, and the expert of every row.
+__global__ __launch_bounds__(1024) void k_row_blocks(ProductArgs a) {
+  __shared__ int s_part[17];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int per = a.E + a.B, total = a.nranks * per;
+  int carry = 0;
+  for (int c0 = 0; c0 < total; c0 += 1024) {
+    const int i = c0 + tid, r = a.first_rank + i / per, j = i % per;
+    int lo = 0, len = 0;
+    if (i < total) {
+      const int32_t* cu = a.cu + int64_t(r) * (per + 1) + j;
+      lo = cu[0];
+      len = cu[1] - lo;
+    }
+    const int n = (len + a.height - 1) / a.height;
+    const int incl = wave_incl_scan(n);
+    if (lane == kWave - 1) s_part[wave] = incl;
+    __syncthreads();
+    if (wave == 0) {
+      const int x = lane < 16 ? s_part[lane] : 0;
+      const int xi = wave_incl_scan(x);
+      if (lane < 16) s_part[lane] = xi - x;
+      if (lane == 15) s_part[16] = xi;
+    }
+    __syncthreads();
+    const int at = carry + s_part[wave] + incl - n;
+    carry += s_part[16];
+    for (int m = 0; m < n && at + m < a.blocks; ++m)
+      a.list[at + m] = RowItem{r, j, r * a.SK + lo + m * a.height,
+                               min(a.height, len - m * a.height), at, n};
+    __syncthreads();
+  }
+  if (tid == 0) *a.nblocks = min(carry, a.blocks);
+}
+
+struct RowBlock {
+  int r, j, row0, rows;                       // rank, weight row, first row (absolute), rows
+  int n0, split;                              // first column, part of the k axis
+};
+
+// What this workgroup multiplies; false: nothing.  Neighbouring items go to one
+// XCD: the row blocks of a band of a segment under one strip of columns, then the
+// next strip, so that what an XCD's units work on at a time is about square and
+// its L2 reads the fewest rows and columns for it.  A segment is cut into even
+// bands of 6 to 11 blocks (65,536 rows of 7,168 onto 2,048: bands of 4, 8, 16 and
+// 32 blocks take 1.70, 1.69, 1.73 and 1.95 ms; over 48 experts of 11 blocks each,
+// bands of 8 that straddle them 1.95 ms, of 11 1.89).
+__device__ __forceinline__ bool my_block(const ProductArgs& a, RowBlock& b) {
+  const int blocks = a.cu ? *a.nblocks : a.blocks;
+  const int units = blocks * a.strips, items = units * a.splits, per = (items + 7) / 8;
+  const int q = blockIdx.x / 8, item = (blockIdx.x % 8) * per + q;
+  if (q >= per || item >= items) return false;
+  b.split = item / units;
+  const int u = item % units;
+  int first = 0, cnt = blocks;
+  if (a.cu) {
+    first = __builtin_amdgcn_readfirstlane(a.list[u / a.strips].first);
+    cnt = __builtin_amdgcn_readfirstlane(a.list[u / a.strips].cnt);
+  }
+  const int bands = max(1, (2 * cnt + kBand) / (2 * kBand));
+  const int size = (cnt + bands - 1) / bands, in = u - first * a.strips;
+  const int band = in / (size * a.strips), at = in % (size * a.strips);
+  const int high = min(size, cnt - band * size), blk = first + band * size + at % high;
+  b.n0 = (at / high) * a.cols;
+  if (a.cu) {
+    b.r = __builtin_amdgcn_readfirstlane(a.list[blk].r);
+    b.j = __builtin_amdgcn_readfirstlane(a.list[blk].j);
+    b.row0 = __builtin_amdgcn_readfirstlane(a.list[blk].row0);
+    b.rows = __builtin_amdgcn_readfirstlane(a.list[blk].rows);
+  } else {
+    b.r = b.j = 0;
+    b.row0 = blk * a.height;
+    b.rows = min(a.height, a.rows - b.row0);
+  }
+  return true;
+}
+
+// Weights of the block's segment, and its share of the steps.
+__device__ __forceinline__ const uint16_t* weights_of(const ProductArgs& a, const RowBlock& b) {
+  const int64_t size = int64_t(a.H) * a.ep.N;
+  return b.j < a.E ? a.w_home + b.j * size : a.w_pref + (int64_t(b.r) * a.B + (b.j - a.E)) * size;
+}
+__device__ __forceinline__ int first_step(const ProductArgs& a, int split) {
+  return int(int64_t(split) * a.steps / a.splits);
+}
+
+// A lane's eight columns of one row: to the workspace, or through the epilogue.
+template <bool SPLIT>
+__device__ __forceinline__ void give8(const ProductArgs& a, const RowBlock& rb, const DropKey& key,
+                                      float (&z)[8], const float (&bias)[8], int m, int n) {
+  const int64_t row = int64_t(rb.row0) + m;
+  if constexpr (SPLIT) {
+    const int64_t at = row - int64_t(a.first_rank) * a.SK;
+    store8(a.partial + (int64_t(rb.split) * a.rows + at) * a.ep.N + n, z);
+    if (a.cu && n == 0 && rb.split == 0)
+      a.row_expert[at] = expert_of(a.ep, rb.r, rb.j, a.E, a.B);
+  } else {
+    epilogue8(a.ep, key, z, bias, row, n);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the single tokens of decoding, the router.  The time is that of
+// reading the weights once, so they go from memory to registers and nowhere else.
+// A wave takes 128 columns and steps of 32 k.  Lane l loads rows k0 + 8 (l / 16) +
+// 0 .. 7 of columns n0 + 8 (l % 16) + 0 .. 7, eight 16-byte loads of which every 16
+// lanes cover 256 contiguous bytes.  A matrix instruction wants eight consecutive
+// k of one column per lane; a lane has an 8 x 8 block, whose transposition is 32
+// byte permutes (pairs of rows; larger strides only rename registers).
+// Instruction i then multiplies columns n0 + 8 (l % 16) + i, and a lane ends with
+// eight consecutive columns of a row: one group of the epilogue.  The four waves
+// of a workgroup share its steps and are joined in LDS.
+// ---------------------------------------------------------------------------
+
+// Columns 2j and 2j + 1 of an 8 x 8 block as eight consecutive k each.
+__device__ __forceinline__ void column_pair(const u32x4 (&w)[8], int j, bf16x8& even,
+                                            bf16x8& odd) {
+  u32x4 e, o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    e[q] = __builtin_amdgcn_perm(w[2 * q + 1][j], w[2 * q][j], 0x05040100u);
+    o[q] = __builtin_amdgcn_perm(w[2 * q + 1][j], w[2 * q][j], 0x07060302u);
+  }
+  even = __builtin_bit_cast(bf16x8, e);
+  odd = __builtin_bit_cast(bf16x8, o);
+}
+
+// RB: blocks of 16 rows that a workgroup takes.
+template <int RB, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
+  __shared__ f32x4 s_sum[4 * 3 * RB * kWave * 2];
+  RowBlock rb;
+  if (!my_block(a, rb)) return;
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int H = a.H, N = a.ep.N, rows = rb.rows;
+  const int n = rb.n0 + 8 * (lane & 15);
+  const char* w = reinterpret_cast<const char*>(weights_of(a, rb));
+  const char* x = reinterpret_cast<const char*>(a.x + int64_t(rb.row0) * H);
+  // rows past the block's and columns past the matrix read the first ones:
+  // what they give is not stored
+  const uint32_t wcol = 2u * (n < N ? n : 0);
+  uint32_t xrow[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int m = 16 * b + (lane & 15);
+    xrow[b] = 2u * uint32_t(m < rows ? m : 0) * H;
+  }
+  f32x4 acc[8][RB];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int t0 = first_step(a, rb.split), t1 = first_step(a, rb.split + 1);
+  auto load = [&](int t, u32x4 (&wr)[8], u32x4 (&xr)[RB]) {
+    const int k = t * kFewStep + 8 * (lane >> 4);
+    const bool in = k < H;
+    const uint32_t wk = wcol + 2u * uint32_t(in ? k : 0) * N;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      wr[q] = *reinterpret_cast<const u32x4*>(w + (wk + 2u * uint32_t(q) * N));
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+      xr[b] = *reinterpret_cast<const u32x4*>(x + (xrow[b] + 2u * uint32_t(in ? k : 0)));
+  };
+  auto multiply = [&](int t, u32x4 (&wr)[8], u32x4 (&xr)[RB]) {
+    if ((t + 1) * kFewStep > H && t * kFewStep + 8 * (lane >> 4) >= H) {
+      // k past the end: zeros on both sides (0 times infinity is none)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) wr[q] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < RB; ++b) xr[b] = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      bf16x8 even, odd;
+      column_pair(wr, jj, even, odd);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const bf16x8 xa = __builtin_bit_cast(bf16x8, xr[b]);
+        acc[2 * jj][b] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, even, acc[2 * jj][b], 0, 0, 0);
+        acc[2 * jj + 1][b] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, odd, acc[2 * jj + 1][b], 0, 0, 0);
+      }
+    }
+  };
+  // two steps in flight
+  u32x4 w0[8], w1[8], x0[RB], x1[RB];
+  int t = t0 + wv;
+  if (t < t1) load(t, w0, x0);
+#pragma unroll 1
+  for (; t < t1; t += 8) {
+    if (t + 4 < t1) load(t + 4, w1, x1);
+    multiply(t, w0, x0);
+    if (t + 4 >= t1) break;
+    if (t + 8 < t1) load(t + 8, w0, x0);
+    multiply(t + 4, w1, x1);
+  }
+
+  // Register v of an accumulator is row 4 (l / 16) + v of its block: wave v
+  // sums those rows of the four waves.
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (v == wv) continue;
+    f32x4* to = s_sum + (v * 3 + (wv < v ? wv : wv - 1)) * RB * kWave * 2;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      to[(b * 2 + 0) * kWave + lane] = f32x4{acc[0][b][v], acc[1][b][v], acc[2][b][v], acc[3][b][v]};
+      to[(b * 2 + 1) * kWave + lane] = f32x4{acc[4][b][v], acc[5][b][v], acc[6][b][v], acc[7][b][v]};
+    }
+  }
+  __syncthreads();
+  float bias[8];
+  DropKey key{};
+  if constexpr (!SPLIT) {
+    bias8(a.ep, expert_of(a.ep, rb.r, rb.j, a.E, a.B), a.E, n, bias);
+    if (a.ep.cut) key = drop_key(a.ep.rng);
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    float z[8];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (v == wv)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = acc[i][b][v];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+      const f32x4* from = s_sum + ((wv * 3 + u) * RB + b) * kWave * 2;
+      const f32x4 lo = from[lane], hi = from[kWave + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[i] += lo[i];
+        z[4 + i] += hi[i];
+      }
+    }
+    const int m = 16 * b + 4 * (lane >> 4) + wv;
+    if (m < rows && n < N) give8<SPLIT>(a, rb, key, z, bias, m, n);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// More rows than weights should be read again for, and fewer than fill the chip
+// with 256 x 256 tiles: 128 x 128 tiles, four waves of 64 x 64 (2 x 2 blocks of
+// 32 x 32), operands straight into LDS in stages of 64 k, the k axis cut over
+// workgroups as above.  Both operands' rows are whole 128- or 256-byte lines: x
+// [128 rows][64 k] is read with 16-byte LDS reads (chunk kc of row m at kc ^ (m /
+// 2) % 8), the weights [64 k][128 columns] with the transposing read (chunk c of
+// row k at c ^ 4 (k % 4)); neither has a bank conflict.  NST stages: four, with a
+// workgroup of the unit's own; or two, with two workgroups whose loads and
+// epilogues cover each other's products.
+// ---------------------------------------------------------------------------
+constexpr int kMidTile = 128, kMidStep = 64;
+constexpr int kMidHalf = kMidTile * kMidStep * 2;      // bytes of one operand's stage
+
+template <bool SPLIT>
+__global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
+  constexpr int NST = 2;
+  static_assert(2 * kMidHalf * NST >= 4 * 64 * 256, "the epilogue's staging fits the stages");
+  __shared__ __attribute__((aligned(1024))) unsigned char s_st[NST * 2 * kMidHalf];
+  RowBlock rb;
+  if (!my_block(a, rb)) return;
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wm = wv >> 1, wn = wv & 1;
+  const int H = a.H, N = a.ep.N, n0 = rb.n0;
+
+  // Fragment reads: x rows 64 wm + 32 i + lane % 32, chunk 2 s + lane / 32; the
+  // weights' pieces as lds_tr wants them (lane / 16 picks k half and column half).
+  const int G4 = lane >> 4, li = lane & 15;
+  int xo[4], wo[2];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int row = wm * 64 + (lane & 31), kc = 2 * s + (lane >> 5);
+    xo[s] = row * 128 + ((kc ^ ((row >> 1) & 7)) << 4);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = (4 * (2 * wn + j) + 2 * (G4 & 1) + ((li & 3) >> 1)) ^ (4 * (li >> 2));
+    wo[j] = (8 * (G4 >> 1) + (li >> 2)) * 256 + c * 16 + 8 * (li & 1);
+  }
+
+  const u32x4 rx = make_rsrc(a.x + int64_t(rb.row0) * H, uint32_t(rb.rows) * H * 2);
+  const u32x4 rw = make_rsrc(weights_of(a, rb), uint32_t(H) * N * 2);
+  const int t0 = first_step(a, rb.split), t1 = first_step(a, rb.split + 1);
+
+  // Load u of this wave: x rows 8 (4 wv + u) + lane / 8, weight rows 4 (4 wv +
+  // u) + lane / 16.  Past the rows, or past k in the last step, an offset
+  // beyond every tensor: zeros.
+  auto issue = [&](int t) {
+    unsigned char* st = s_st + (t % NST) * 2 * kMidHalf;
+    const bool ragged = (t + 1) * kMidStep > H;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int p = wv * 4 + u;
+      const int row = 8 * p + (lane >> 3), kc = (lane & 7) ^ ((row >> 1) & 7);
+      uint32_t vx = 2u * uint32_t(row) * H + kc * 16;
+      const int k = 4 * p + G4, c = li ^ (4 * G4);
+      uint32_t vw = 2u * (uint32_t(k) * N + n0 + 8 * c);
+      if (ragged) {
+        if (t * kMidStep + 8 * kc >= H) vx = 0xfffffff0u;
+        if (t * kMidStep + k >= H) vw = 0xfffffff0u;
+      }
+      if (row >= rb.rows) vx = 0xfffffff0u;
+      load_lds16(rx, st + p * 1024, vx, uint32_t(t) * kMidStep * 2);
+      load_lds16(rw, st + kMidHalf + p * 1024, vw, uint32_t(t) * kMidStep * 2 * N);
+    }
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s)
+    if (t0 + s < t1) issue(t0 + s);
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    // this wave's loads of stage t have landed; the barrier makes every wave's
+    // visible, and says that all are done with the stage that is filled next
+    wait_vm<0>();
+    // its own LDS reads of the last step are done too, not only asked for
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + NST - 1 < t1) issue(t + NST - 1);
+    const unsigned char* xs = s_st + (t % NST) * 2 * kMidHalf;
+    const unsigned char* ws = xs + kMidHalf;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      bf16x8 xa[2], wb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        xa[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(xs + xo[s] + i * 4096));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned char* p = ws + wo[j] + s * 16 * 256;
+        wb[j] = join(lds_tr(p), lds_tr(p + 4 * 256));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], wb[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  __syncthreads();
+
+  // 32 x 32 accumulators: lane l holds column l % 32, rows 8 (v / 4) + 4 (l /
+  // 32) + v % 4.  Staged in the wave's own 16 KB as 64 rows of 256 bytes (the
+  // lane halves, 4 rows apart, swap the row's two column blocks: other banks).
+  unsigned char* cs = s_st + wv * 16384;
+  const int half = lane >> 5;
+  float bias[2] = {0.f, 0.f};
+  DropKey key{};
+  if constexpr (!SPLIT) {
+    const int e = expert_of(a.ep, rb.r, rb.j, a.E, a.B);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bias[j] = bias1(a.ep, e, a.E, n0 + wn * 64 + 32 * j + (lane & 31));
+    if (a.ep.cut) key = drop_key(a.ep.rng);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        *reinterpret_cast<float*>(cs + (32 * i + 8 * (v >> 2) + 4 * half + (v & 3)) * 256 +
+                                  ((j ^ half) * 128) + (lane & 31) * 4) = acc[i][j][v] + bias[j];
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  const int n = n0 + wn * 64 + (lane & 7) * 8;
+  auto place = [&](int k, int64_t& at) -> float* {
+    const int rr = 8 * k + (lane >> 3), m = wm * 64 + rr;
+    if (m >= rb.rows || n >= N) return nullptr;
+    at = (int64_t(rb.row0) + m) * N + n;
+    const int blk = ((lane & 7) >> 2) ^ ((rr >> 2) & 1);
+    return reinterpret_cast<float*>(cs + rr * 256 + blk * 128 + (lane & 3) * 32);
+  };
+  if constexpr (SPLIT) {
+    const int64_t first = int64_t(a.first_rank) * a.SK;
+    float* to = a.partial + (int64_t(rb.split) * a.rows - first) * N;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      int64_t at = 0;
+      const float* p = place(k, at);
+      if (!p) continue;
+      float z[8];
+      load8(p, z);
+      store8(to + at, z);
+    }
+    if (a.cu && rb.split == 0 && n0 == 0 && wn == 0 && wm * 64 + lane < rb.rows)
+      a.row_expert[rb.row0 - first + wm * 64 + lane] = expert_of(a.ep, rb.r, rb.j, a.E, a.B);
+  } else {
+    epilogue_block(a.ep, key, place);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: 128 x 256 tiles, four waves of 64 x 128 (2 x 4 blocks), two
+// workgroups on a unit, so that one's loads and epilogue are covered by the
+// other's products.  LDS bandwidth sets the pace: a tile of this shape reads and
+// fills 72 KB for every 32 k, 1.1 times what the matrix pipe needs to be fed; 128
+// x 128 1.5 times.  The weights go through three stages of 32 k (rows of 512
+// bytes); x, whose rows of 32 k would be half lines, in pairs of steps through
+// two buffers: 80 KB a workgroup.
+// ---------------------------------------------------------------------------
+constexpr int kWideCols = 256, kWideStep = 32;
+constexpr int kWidePair = 128 * 64 * 2, kWideW = kWideStep * kWideCols * 2;
+
+template <bool SPLIT>
+__global__ __launch_bounds__(256, 2) void k_wide(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) unsigned char s_x[2 * kWidePair];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_w[3 * kWideW];
+  RowBlock rb;
+  if (!my_block(a, rb)) return;
+  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wm = wv >> 1, wn = wv & 1;
+  const int H = a.H, N = a.ep.N, n0 = rb.n0;
+  const int G4 = lane >> 4, li = lane & 15;
+  int xo[4], wo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int row = wm * 64 + (lane & 31), kc = 2 * s + (lane >> 5);
+    xo[s] = row * 128 + ((kc ^ ((row >> 1) & 7)) << 4);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = (4 * (4 * wn + j) + 2 * (G4 & 1) + ((li & 3) >> 1)) ^ (4 * (li >> 2));
+    wo[j] = (8 * (G4 >> 1) + (li >> 2)) * 512 + c * 16 + 8 * (li & 1);
+  }
+  const u32x4 rx = make_rsrc(a.x + int64_t(rb.row0) * H, uint32_t(rb.rows) * H * 2);
+  const u32x4 rw = make_rsrc(weights_of(a, rb), uint32_t(H) * N * 2);
+  // whole pairs of steps: the parts of the k axis are cut at multiples of 64
+  const int p0 = first_step(a, rb.split), p1 = first_step(a, rb.split + 1);
+  const int t0 = 2 * p0, t1 = min(2 * p1, (H + kWideStep - 1) / kWideStep);
+
+  // Load u of this wave: x rows 8 (4 wv + u) + lane / 8, weight rows 2 (4 wv + u)
+  // + lane / 32 of a step.  Past the rows or past k an offset beyond every
+  // tensor: zeros.
+  uint32_t vx[4], vw[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int p = wv * 4 + u;
+    const int row = 8 * p + (lane >> 3), kc = (lane & 7) ^ ((row >> 1) & 7);
+    vx[u] = row < rb.rows ? 2u * uint32_t(row) * H + kc * 16 : 0xfffffff0u;
+    const int k = 2 * p + (lane >> 5), c = (lane & 31) ^ (4 * (k & 3));
+    vw[u] = 2u * (uint32_t(k) * N + n0 + 8 * c);
+  }
+  auto issue_x = [&](int pair) {
+    unsigned char* to = s_x + (pair & 1) * kWidePair + wv * 4096;
+    const bool ragged = (pair + 1) * 64 > H;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 8 * (wv * 4 + u) + (lane >> 3), kc = (lane & 7) ^ ((row >> 1) & 7);
+      const uint32_t v = ragged && pair * 64 + 8 * kc >= H ? 0xfffffff0u : vx[u];
+      load_lds16(rx, to + u * 1024, v, uint32_t(pair) * 128);
+    }
+  };
+  auto issue_w = [&](int t) {
+    unsigned char* to = s_w + (t % 3) * kWideW + wv * 4096;
+    const bool ragged = (t + 1) * kWideStep > H;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = 2 * (wv * 4 + u) + (lane >> 5);
+      const uint32_t v = ragged && t * kWideStep + k >= H ? 0xfffffff0u : vw[u];
+      load_lds16(rw, to + u * 1024, v, uint32_t(t) * kWideStep * 2 * N);
+    }
+  };
+  f32x16 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  // Order of the loads: x0 w0 w1 | w2 x1 | w3 | w4 x2 | w5 ...: at an even step the
+  // weights of one more step may be in flight, at an odd one those and a pair of x.
+  auto step = [&](int t, auto ODD_) {
+    constexpr int ODD = decltype(ODD_)::value;
+    if (t + 1 >= t1) wait_vm<0>();
+    else if (ODD) wait_vm<8>();
+    else wait_vm<4>();
+    // every wave's loads are visible and its LDS reads of the last step done
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + 2 < t1) {
+      issue_w(t + 2);
+      if (!ODD) issue_x(t / 2 + 1);
+    }
+    const unsigned char* xs = s_x + ((t >> 1) & 1) * kWidePair;
+    const unsigned char* ws = s_w + (t % 3) * kWideW;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8 xa[2], wb[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        xa[i] = __builtin_bit_cast(
+            bf16x8, *reinterpret_cast<const u32x4*>(xs + xo[2 * ODD + s] + i * 4096));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned char* p = ws + wo[j] + s * 16 * 512;
+        wb[j] = join(lds_tr(p), lds_tr(p + 4 * 512));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[i], wb[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  if (t0 < t1) {
+    issue_x(t0 / 2);
+    issue_w(t0);
+    if (t0 + 1 < t1) issue_w(t0 + 1);
+  }
+#pragma unroll 1
+  for (int t = t0; t < t1; t += 2) {
+    step(t, std::integral_constant<int, 0>());
+    if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>());
+  }
+  __syncthreads();
+
+  // Two passes of 32 rows x 128 columns staged in the wave's own 16 KB, rows of
+  // 512 bytes (of two neighbouring blocks of 32 columns the lane halves write one
+  // each: other banks).
+  unsigned char* cs = wv < 2 ? s_x + wv * 16384 : s_w + (wv - 2) * 16384;
+  const int half = lane >> 5, n = n0 + wn * 128 + li * 8;
+  const int e = expert_of(a.ep, rb.r, rb.j, a.E, a.B);
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  DropKey key{};
+  if constexpr (!SPLIT) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = bias1(a.ep, e, a.E, n0 + wn * 128 + 32 * j + (lane & 31));
+    if (a.ep.cut) key = drop_key(a.ep.rng);
+  }
+  const int64_t first = int64_t(a.first_rank) * a.SK;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (wm * 64 + 32 * i >= rb.rows) break;                // uniform: no row is left
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        *reinterpret_cast<float*>(cs + (8 * (v >> 2) + 4 * half + (v & 3)) * 512 +
+                                  ((j ^ half) * 128) + (lane & 31) * 4) = acc[i][j][v] + bias[j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    auto place = [&](int k, int64_t& at) -> float* {
+      const int rr = 4 * k + G4, m = wm * 64 + 32 * i + rr;
+      if (m >= rb.rows || n >= N) return nullptr;
+      at = (int64_t(rb.row0) + m) * N + n;
+      const int blk = (li >> 2) ^ ((rr >> 2) & 1);
+      return reinterpret_cast<float*>(cs + rr * 512 + blk * 128 + (lane & 3) * 32);
+    };
+    if constexpr (SPLIT) {
+      float* to = a.partial + (int64_t(rb.split) * a.rows - first) * N;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        int64_t at = 0;
+        const float* p = place(k, at);
+        if (!p) continue;
+        float z[8];
+        load8(p, z);
+        store8(to + at, z);
+      }
+    } else {
+      epilogue_block(a.ep, key, place);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  if (SPLIT && a.cu && rb.split == 0 && n0 == 0 && wn == 0 && wm * 64 + lane < rb.rows)
+    a.row_expert[rb.row0 - first + wm * 64 + lane] = e;
+}
+
+// Sums of the splits in ascending order, and the epilogue.
+__global__ __launch_bounds__(256) void k_join(ProductArgs a) {
+  const int64_t nv = a.ep.N / 8, g = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (g >= nv * a.rows) return;
+  const int64_t at = g / nv;
+  const int n = int(g % nv) * 8;
+  DropKey key{};
+  if (a.ep.cut) key = drop_key(a.ep.rng);
+  float b[8];
+  bias8(a.ep, a.cu ? a.row_expert[at] : 0, a.E, n, b);
+  float z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = 0.f;
+  const float* p = a.partial + at * a.ep.N + n;
+#pragma unroll 8
+  for (int s = 0; s < a.splits; ++s) {
+    float v[8];
+    load8(p + int64_t(s) * a.rows * a.ep.N, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += v[i];
+  }
+  epilogue8(a.ep, key, z, b, at + int64_t(a.first_rank) * a.SK, n);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+// The four kernels: rows and columns of a workgroup's tile, k of a step, the
+// waves that share the steps, the workgroups that the chip holds at a time, and
+// the terms of a call's time in microseconds:
+//   start + steps * (rounds * steps of a wave) + rounds * round
+//     + filled * (steps of a wave * workgroups / those at a time) + store * outputs / 2^20
+// with a last round of at most half as many workgroups at kHalfRound (tiles in
+// LDS; the others overlap their rounds).  If the k axis is split, join more and
+// sums * 2^-20 for each value of the partial sums; grouped calls add list.
+// Fitted (non-negative least squares of the relative error) to 1,850 timings of
+// 86 shapes on one MI355X, one to 65,536 rows, widths of 64 to 7,168, one to 384
+// experts: the median error is 5 %, and what the model picks was 3 % slower than
+// the best of them on average, 24 % at worst.
+struct Tile {
+  int height, cols, step, waves, at_once;
+  float start, steps, round, filled, join, sums, store, list;
+};
+constexpr Tile kTiles[4] = {
+    {16, kFewCols, kFewStep, 4, 768, 3.54f, 0.386f, 0.689f, 1.05f, 2.68f, 2.12f, 0.53f, 3.25f},
+    {32, kFewCols, kFewStep, 4, 512, 4.22f, 0.434f, 0.399f, 0.675f, 2.61f, 2.17f, 1.03f, 3.28f},
+    {kMidTile, kMidTile, kMidStep, 1, 512, 5.24f, 0.886f, 0.f, 0.f, 2.54f, 1.90f, 0.67f, 2.96f},
+    {kMidTile, kWideCols, kMidStep, 1, 512, 6.29f, 1.555f, 0.f, 0.f, 2.57f, 1.49f, 0.70f, 2.87f},
+};
+constexpr float kHalfRound = 0.65f;
+constexpr int kMostSplits = 32;          // parts of the k axis
+constexpr int64_t kMostItems = 1 << 24;  // a launch holds fewer than 2^32 threads
+constexpr int64_t kSplitItems = 512;     // a split call fills the chip about once
+
+// Everything that the host decides about a call, from its configuration alone.
+struct ProductPlan {
+  int64_t rows;
+  int tile, blocks, strips, steps, splits;
+};
+
+static ProductPlan product_plan(const moe_cfg* c, bool dense, int64_t nranks) {
+  ProductPlan best{};
+  best.rows = nranks * c->S * c->K;
+  // segments that may have rows: each costs a block that is not full
+  const int64_t live = dense ? 0 : std::min(nranks * (c->E + c->B), best.rows);
+  const float out = float(best.rows) * c->Hp / (1 << 20);
+  float least = INFINITY;
+  for (int k = 0; k < 4; ++k) {
+    const Tile& t = kTiles[k];
+    const int64_t blocks = (best.rows + t.height - 1) / t.height + live;
+    const int64_t strips = (c->Hp + t.cols - 1) / t.cols, steps = (c->H + t.step - 1) / t.step;
+    if (blocks * strips >= kMostItems) continue;
+    for (int p = 1; p <= kMostSplits; p += p < 4 ? 1 : p < 8 ? 2 : p < 16 ? 4 : 8) {
+      if (p > 1 && (p > steps || blocks * strips * p > kSplitItems * (k < 2 ? 4 : 1))) break;
+      const int64_t items = blocks * strips * p, n = ((steps + p - 1) / p + t.waves - 1) / t.waves;
+      float rounds = float(items) / t.at_once;
+      if (t.waves == 1) {
+        const int64_t rest = items % t.at_once;
+        rounds = float(items / t.at_once);
+        rounds += rest == 0 ? 0.f : rest <= t.at_once / 2 ? kHalfRound : 1.f;
+      } else if (rounds < 1.f) {
+        rounds = 1.f;
+      }
+      float time = t.start + rounds * (t.steps * n + t.round) + t.filled * n * items / t.at_once;
+      time += t.store * out + (p > 1 ? t.join + t.sums * p * out : 0.f) + (dense ? 0.f : t.list);
+      if (time < least) {
+        least = time;
+        best.tile = k; best.blocks = int(blocks); best.strips = int(strips);
+        best.steps = int(steps); best.splits = p;
+      }
+    }
+  }
+  return best;
+}
+
+// Workspace of any ranks of a configuration: the number of blocks, their list,
+// the rows' experts and the sums, each the most that a plan can want.
+static int64_t most_blocks(const moe_cfg* c) {
+  const int64_t rows = int64_t(c->R) * c->S * c->K;
+  return (rows + 15) / 16 + std::min(int64_t(c->R) * (c->E + c->B), rows);
+}
+static size_t expert_at(const moe_cfg* c) {
+  return 256 + align256(size_t(most_blocks(c)) * sizeof(RowItem));
+}
+static size_t sums_at(const moe_cfg* c) {
+  return expert_at(c) + align256(size_t(c->R) * c->S * c->K * 4);
+}
+size_t product_ws_bytes(const moe_cfg* c) {
+  const int64_t each = int64_t(c->R) * c->S * c->K * c->Hp * kMostSplits;
+  return sums_at(c) + size_t(std::min(each, kSplitItems * kMidTile * kWideCols)) * 4;
+}
+
+// One workspace for the product with an epilogue and for the epilogue's backward.
+static size_t epilogue_ws_bytes(const moe_cfg* c) {
+  return std::max(product_ws_bytes(c), epilogue_bwd_ws_bytes(c));
+}
+
+template <bool SPLIT>
+static void run_product(const ProductArgs& a, int tile, hipStream_t stream) {
+  const int64_t items = int64_t(a.blocks) * a.strips * a.splits;
+  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(256);
+  if (tile == 0) hipLaunchKernelGGL((k_few<1, SPLIT>), grid, block, 0, stream, a);
+  else if (tile == 1) hipLaunchKernelGGL((k_few<2, SPLIT>), grid, block, 0, stream, a);
+  else if (tile == 2) hipLaunchKernelGGL((k_mid<SPLIT>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_wide<SPLIT>), grid, block, 0, stream, a);
+}
+
+}  // namespace moonep
+
+using namespace moonep;
+
+extern "C" int moe_epilogue_workspace_size(const moe_cfg* cfg, const moe_epilogue_cfg* ec,
+                                           size_t* bytes_out) {
+  const int rc = check_cfg(cfg);
+  if (rc != MOE_OK) return rc;
+  if (!valid_epilogue(ec) || !bytes_out) return MOE_EINVAL;
+  *bytes_out = epilogue_ws_bytes(cfg);
+  return MOE_OK;
+}
+
+extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_cfg* ec,
+                                         const moe_plan* plan, const moe_bf16* xperm,
+                                         const moe_bf16* w_home, const moe_bf16* w_pref,
+                                         const float* bias, const void* residual,
+                                         const int64_t* rng, void* y, moe_bf16* pre,
+                                         int32_t rank_begin, int32_t rank_end, void* workspace,
+                                         hipStream_t stream) {
+  const int rc = check_cfg(cfg);
+  if (rc != MOE_OK) return rc;
+  if (!valid_epilogue(ec)) return MOE_EINVAL;
+  if (rank_begin < 0 || rank_end > cfg->R || rank_begin > rank_end) return MOE_EINVAL;
+  if (!plan && !one_matrix(cfg)) return MOE_EINVAL;
+  if (rank_begin == rank_end || cfg->S == 0) return MOE_OK;
+  ProductArgs a{};
+  Epilogue& ep = a.ep;
+  drop_params(ec->p, &ep.cut, &ep.scale);
+  const bool slots = plan && cfg->B > 0;
+  if (!xperm || !w_home || !y || !workspace || (ep.cut && !rng)) return MOE_EINVAL;
+  if (plan && !plan->cu_seqlens) return MOE_EINVAL;
+  if (slots && (!w_pref || !plan->slot_expert)) return MOE_EINVAL;
+  if (!aligned16(xperm, w_home, slots ? w_pref : nullptr, bias, residual, y, pre, workspace))
+    return MOE_EINVAL;
+  // the listed ranks' parts of every tensor
+  const int64_t SK = int64_t(cfg->S) * cfg->K, first = rank_begin * SK;
+  const int64_t nr = rank_end - rank_begin, rows = nr * SK, segs = cfg->E + cfg->B;
+  const int64_t out = cfg->Hp * (ec->f32 ? 4 : 2), w = int64_t(cfg->H) * cfg->Hp * 2;
+  const int64_t ws = (int64_t)epilogue_ws_bytes(cfg);
+  const char* yb = static_cast<const char*>(y) + first * out;
+  const char* rb = residual ? static_cast<const char*>(residual) + first * out : nullptr;
+  const moe_bf16* pb = pre ? pre + first * cfg->Hp : nullptr;
+  if (clash({{yb, rows * out}, {pb, rows * cfg->Hp * 2}, {workspace, ws}},
+            {{xperm + first * cfg->H, rows * cfg->H * 2},
+             {w_home, cfg->E * w},
+             {slots ? w_pref + int64_t(rank_begin) * cfg->B * (w / 2) : nullptr, nr * cfg->B * w},
+             {plan ? plan->cu_seqlens + rank_begin * (segs + 1) : nullptr, nr * (segs + 1) * 4},
+             {slots ? plan->slot_expert : nullptr, int64_t(cfg->R) * cfg->B * 4},
+             {bias, int64_t(cfg->E) * cfg->Hp * 4},
+             {rb == yb ? nullptr : rb, rows * out},
+             {ep.cut ? rng : nullptr, 16}}) ||
+      clash({{pb, rows * cfg->Hp * 2}, {workspace, ws}}, {{rb, rows * out}}))
+    return MOE_EINVAL;
+  const ProductPlan p = product_plan(cfg, !plan, nr);
+  if (p.splits == 0) return MOE_ELIMIT;
+  ep.bias = bias; ep.residual = residual; ep.rng = ep.cut ? rng : nullptr; ep.y = y; ep.pre = pre;
+  ep.slot_expert = slots ? plan->slot_expert : nullptr;
+  ep.act = ec->act; ep.f32 = ec->f32; ep.N = cfg->Hp;
+  a.x = xperm; a.w_home = w_home; a.w_pref = w_pref; a.cu = plan ? plan->cu_seqlens : nullptr;
+  a.H = cfg->H; a.E = cfg->E; a.B = cfg->B; a.SK = (int32_t)SK;
+  a.first_rank = rank_begin; a.nranks = (int32_t)nr; a.rows = (int32_t)p.rows;
+  a.height = kTiles[p.tile].height; a.cols = kTiles[p.tile].cols;
+  a.blocks = p.blocks; a.strips = p.strips; a.steps = p.steps; a.splits = p.splits;
+  char* at = static_cast<char*>(workspace);
+  a.nblocks = reinterpret_cast<int32_t*>(at);
+  a.list = reinterpret_cast<RowItem*>(at + 256);
+  a.row_expert = reinterpret_cast<int32_t*>(at + expert_at(cfg));
+  a.partial = reinterpret_cast<float*>(at + sums_at(cfg));
+  if (plan) hipLaunchKernelGGL(k_row_blocks, dim3(1), dim3(1024), 0, stream, a);
+  if (p.splits == 1) {
+    run_product<false>(a, p.tile, stream);
+  } else {
+    run_product<true>(a, p.tile, stream);
+    const int64_t groups = p.rows * (cfg->Hp / 8);
+    hipLaunchKernelGGL(k_join, dim3((unsigned)((groups + 255) / 256)), dim3(256), 0, stream, a);
+  }
+  return hip_status();
+}
