@@ -169,6 +169,34 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// The same past the caches, for tensors that a pass reads or writes once: a
+// stream that stays in the caches costs the others their place (65,536 x 7,168
+// dropped and added, bf16: 0.488 ms through them, 0.446 past them).
+__device__ __forceinline__ void load8_once(const uint16_t* p, float (&v)[8]) {
+  const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    v[2 * q] = bf16_lo(w[q]);
+    v[2 * q + 1] = bf16_hi(w[q]);
+  }
+}
+__device__ __forceinline__ void load8_once(const float* p, float (&v)[8]) {
+  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + 4));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    v[q] = a[q];
+    v[4 + q] = b[q];
+  }
+}
+__device__ __forceinline__ void store8_once(uint16_t* p, const float (&v)[8]) {
+  __builtin_nontemporal_store(round8(v), reinterpret_cast<u32x4*>(p));
+}
+__device__ __forceinline__ void store8_once(float* p, const float (&v)[8]) {
+  __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
+}
+
 // One launch's epilogue.  All rows have N columns.
 struct Epilogue {
   const float* bias;          // [E][N] or null

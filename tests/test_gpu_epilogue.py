@@ -471,6 +471,6 @@ def test_many_rows():
             want += d.sum(0)
             mag = mag + d.abs().sum(0)
         # each term off by its rounding, and one step of fp32 for each addition of a path: a
-        # piece's rows (64 and 3) and the pieces of a rank over eight lanes (rows / 2048 and 8)
-        bound = (2.0 ** -8 * 1.01 + 2 * (80 + per // 2048) * h) * mag
+        # chunk's rows (64 and 3) and the chunks of a rank over 16 lanes (rows / 4096 and 15)
+        bound = (2.0 ** -8 * 1.01 + 2 * (90 + per // 2048) * h) * mag
         close(db[r].double().cpu().numpy(), want.cpu().numpy(), bound.cpu().numpy(), "dbias")
