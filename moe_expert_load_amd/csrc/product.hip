@@ -1,8 +1,8 @@
 // Products of rows with one matrix or with one per expert, and the epilogue
 // (epilogue.hpp), in four kernels by the height of their tiles; the time of each
 // is modelled on the host (kTiles) and the shortest taken.  The grid covers the
-// tiles that a configuration can have; which there are is listed on the device
-// from cu_seqlens (k_row_blocks).  Where the tiles would leave units idle the k
+// tiles that a configuration can have; which there are is found on the device from
+// cu_seqlens (my_block).  Where the tiles would leave units idle the k
 // axis is cut into parts whose sums go to the workspace in fp32; k_join adds them
 // in a fixed order and applies the epilogue.
 #include <math.h>
@@ -21,10 +21,11 @@ namespace moonep {
 constexpr int kFewCols = 128;        // columns of a wave
 constexpr int kFewStep = 32;         // k of a step
 constexpr int kBand = 8;             // row blocks of a band, about
+constexpr int kScan = 8;             // segments a lane looks at, without a list
 
 struct RowItem {
-  int32_t r, j, row0, rows;  // rank, weight row, first row (absolute), rows
-  int32_t first, cnt;        // its segment's first item, and how many there are
+  int32_t seg;               // segment, counted from the first listed rank's first
+  int32_t first, cnt;        // the segment's first item, and how many there are
 };
 
 struct ProductArgs {
@@ -35,27 +36,25 @@ struct ProductArgs {
   float* partial;            // [splits][rows][N]
   int32_t* nblocks;          // grouped: how many of `list` there are
   int32_t* row_expert;       // [rows], grouped
-  RowItem* list;             // grouped
+  RowItem* list;             // grouped, over more than 64 kScan segments
   int32_t H, E, B, SK, first_rank, nranks;
   int32_t rows, height, cols, strips, steps, splits;
   int32_t blocks;            // grouped: the most there may be
   Epilogue ep;
 };
 
-// The listed ranks' segments as blocks of at most a.height rows, in layout
-// order, and the expert of every row.
+// The listed ranks' segments as blocks of at most a.height rows, in layout order.
 __global__ __launch_bounds__(1024) void k_row_blocks(ProductArgs a) {
   __shared__ int s_part[17];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   const int per = a.E + a.B, total = a.nranks * per;
   int carry = 0;
   for (int c0 = 0; c0 < total; c0 += 1024) {
-    const int i = c0 + tid, r = a.first_rank + i / per, j = i % per;
-    int lo = 0, len = 0;
+    const int i = c0 + tid;
+    int len = 0;
     if (i < total) {
-      const int32_t* cu = a.cu + int64_t(r) * (per + 1) + j;
-      lo = cu[0];
-      len = cu[1] - lo;
+      const int32_t* cu = a.cu + int64_t(a.first_rank + i / per) * (per + 1) + i % per;
+      len = cu[1] - cu[0];
     }
     const int n = (len + a.height - 1) / a.height;
     const int incl = wave_incl_scan(n);
@@ -71,8 +70,7 @@ __global__ __launch_bounds__(1024) void k_row_blocks(ProductArgs a) {
     const int at = carry + s_part[wave] + incl - n;
     carry += s_part[16];
     for (int m = 0; m < n && at + m < a.blocks; ++m)
-      a.list[at + m] = RowItem{r, j, r * a.SK + lo + m * a.height,
-                               min(a.height, len - m * a.height), at, n};
+      a.list[at + m] = RowItem{i, at, n};
     __syncthreads();
   }
   if (tid == 0) *a.nblocks = min(carry, a.blocks);
@@ -90,32 +88,71 @@ struct RowBlock {
 // bands of 6 to 11 blocks (65,536 rows of 7,168 onto 2,048: bands of 4, 8, 16 and
 // 32 blocks take 1.70, 1.69, 1.73 and 1.95 ms; over 48 experts of 11 blocks each,
 // bands of 8 that straddle them 1.95 ms, of 11 1.89).
+//
+// Where the segments are few every wave counts their blocks itself, kScan
+// segments a lane: 1 us, where the list of k_row_blocks costs 4 and a launch.
 __device__ __forceinline__ bool my_block(const ProductArgs& a, RowBlock& b) {
-  const int blocks = a.cu ? *a.nblocks : a.blocks;
-  const int units = blocks * a.strips, items = units * a.splits, per = (items + 7) / 8;
-  const int q = blockIdx.x / 8, item = (blockIdx.x % 8) * per + q;
-  if (q >= per || item >= items) return false;
+  const int lane = lane_id(), per = a.E + a.B, total = a.nranks * per;
+  const bool scan = a.cu && !a.list;
+  int start[kScan], n[kScan], blocks = a.blocks;
+  if (scan) {
+    blocks = 0;
+#pragma unroll
+    for (int q = 0; q < kScan; ++q) {
+      const int i = q * kWave + lane;
+      n[q] = 0;
+      if (i < total) {
+        const int32_t* cu = a.cu + int64_t(a.first_rank + i / per) * (per + 1) + i % per;
+        n[q] = (cu[1] - cu[0] + a.height - 1) / a.height;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kScan; ++q) {
+      const int incl = wave_incl_scan(n[q]);
+      start[q] = blocks + incl - n[q];
+      blocks += wave_bcast(incl, kWave - 1);
+    }
+  } else if (a.cu) {
+    blocks = *a.nblocks;
+  }
+  const int units = blocks * a.strips, items = units * a.splits, share = (items + 7) / 8;
+  const int place = blockIdx.x / 8, item = (blockIdx.x % 8) * share + place;
+  if (place >= share || item >= items) return false;
   b.split = item / units;
-  const int u = item % units;
-  int first = 0, cnt = blocks;
-  if (a.cu) {
-    first = __builtin_amdgcn_readfirstlane(a.list[u / a.strips].first);
-    cnt = __builtin_amdgcn_readfirstlane(a.list[u / a.strips].cnt);
+  const int u = item % units, near = u / a.strips;         // a block of the same segment
+  int first = 0, cnt = blocks, seg = 0;
+  if (scan) {
+#pragma unroll
+    for (int q = 0; q < kScan; ++q) {
+      const uint64_t hit = __ballot(near >= start[q] && near < start[q] + n[q]);
+      if (hit) {
+        const int src = __ffsll((unsigned long long)hit) - 1;
+        first = wave_bcast(start[q], src);
+        cnt = wave_bcast(n[q], src);
+        seg = q * kWave + src;
+      }
+    }
+  } else if (a.cu) {
+    first = __builtin_amdgcn_readfirstlane(a.list[near].first);
+    cnt = __builtin_amdgcn_readfirstlane(a.list[near].cnt);
+    seg = __builtin_amdgcn_readfirstlane(a.list[near].seg);
   }
   const int bands = max(1, (2 * cnt + kBand) / (2 * kBand));
   const int size = (cnt + bands - 1) / bands, in = u - first * a.strips;
   const int band = in / (size * a.strips), at = in % (size * a.strips);
-  const int high = min(size, cnt - band * size), blk = first + band * size + at % high;
+  const int high = min(size, cnt - band * size), m = (band * size + at % high) * a.height;
   b.n0 = (at / high) * a.cols;
   if (a.cu) {
-    b.r = __builtin_amdgcn_readfirstlane(a.list[blk].r);
-    b.j = __builtin_amdgcn_readfirstlane(a.list[blk].j);
-    b.row0 = __builtin_amdgcn_readfirstlane(a.list[blk].row0);
-    b.rows = __builtin_amdgcn_readfirstlane(a.list[blk].rows);
+    b.r = a.first_rank + seg / per;
+    b.j = seg % per;
+    const int32_t* cu = a.cu + int64_t(b.r) * (per + 1) + b.j;
+    const int lo = cu[0], len = cu[1] - lo;
+    b.row0 = b.r * a.SK + lo + m;
+    b.rows = min(a.height, len - m);
   } else {
     b.r = b.j = 0;
-    b.row0 = blk * a.height;
-    b.rows = min(a.height, a.rows - b.row0);
+    b.row0 = m;
+    b.rows = min(a.height, a.rows - m);
   }
   return true;
 }
@@ -636,12 +673,16 @@ __global__ __launch_bounds__(256) void k_join(ProductArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] = 0.f;
   const float* p = a.partial + at * a.ep.N + n;
-#pragma unroll 8
-  for (int s = 0; s < a.splits; ++s) {
-    float v[8];
-    load8(p + int64_t(s) * a.rows * a.ep.N, v);
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    float v[8][8];                                  // eight parts in flight
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += v[i];
+    for (int s = 0; s < 8; ++s)
+      load8(p + int64_t(min(s0 + s, a.splits - 1)) * a.rows * a.ep.N, v[s]);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < a.splits)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += v[s][i];
   }
   epilogue8(a.ep, key, z, b, at + int64_t(a.first_rank) * a.SK, n);
 }
@@ -652,27 +693,31 @@ __global__ __launch_bounds__(256) void k_join(ProductArgs a) {
 
 // The four kernels: rows and columns of a workgroup's tile, k of a step, the
 // waves that share the steps, the workgroups that the chip holds at a time, and
-// the terms of a call's time in microseconds:
-//   start + steps * (rounds * steps of a wave) + rounds * round
-//     + filled * (steps of a wave * workgroups / those at a time) + store * outputs / 2^20
-// with a last round of at most half as many workgroups at kHalfRound (tiles in
-// LDS; the others overlap their rounds).  If the k axis is split, join more and
-// sums * 2^-20 for each value of the partial sums; grouped calls add list.
-// Fitted (non-negative least squares of the relative error) to 1,850 timings of
-// 86 shapes on one MI355X, one to 65,536 rows, widths of 64 to 7,168, one to 384
-// experts: the median error is 5 %, and what the model picks was 3 % slower than
-// the best of them on average, 24 % at worst.
+// the terms of a call's time in microseconds: with n steps of a wave,
+//   start + rounds * (n * step + round) + halves * (n * half + round)
+//     + n * items / at_once * filled + outputs / 2^20 * store
+// where `halves` is 1 for a last round of at most half as many workgroups as fit
+// (tiles in LDS; the others count it whole), and
+//   + join + parts * part + parts * outputs / 2^20 * sums    if k is cut into parts,
+//   + list + weights of the segments with rows / 2^20 * weight    for experts.
+// Fitted (non-negative least squares of the relative error) to 8,011 timings of
+// 406 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
+// 7,168, one to 384 experts.  The median error is 4 %; what the model picks was
+// 1.7 % slower than the best of them on average, 25 % at worst.
 struct Tile {
-  int height, cols, step, waves, at_once;
-  float start, steps, round, filled, join, sums, store, list;
+  int height, cols, step_k, waves, at_once;
+  float start, step, half, round, filled, join, part, sums, store, list, weight;
 };
 constexpr Tile kTiles[4] = {
-    {16, kFewCols, kFewStep, 4, 768, 3.54f, 0.386f, 0.689f, 1.05f, 2.68f, 2.12f, 0.53f, 3.25f},
-    {32, kFewCols, kFewStep, 4, 512, 4.22f, 0.434f, 0.399f, 0.675f, 2.61f, 2.17f, 1.03f, 3.28f},
-    {kMidTile, kMidTile, kMidStep, 1, 512, 5.24f, 0.886f, 0.f, 0.f, 2.54f, 1.90f, 0.67f, 2.96f},
-    {kMidTile, kWideCols, kMidStep, 1, 512, 6.29f, 1.555f, 0.f, 0.f, 2.57f, 1.49f, 0.70f, 2.87f},
+    {16, kFewCols, kFewStep, 4, 768,
+     3.80f, 0.402f, 0.f, 0.643f, 0.803f, 2.14f, 0.065f, 2.34f, 0.89f, 1.06f, 0.036f},
+    {32, kFewCols, kFewStep, 4, 512,
+     3.77f, 0.429f, 0.f, 1.12f, 0.564f, 2.09f, 0.062f, 2.03f, 0.89f, 1.10f, 0.018f},
+    {kMidTile, kMidTile, kMidStep, 1, 512,
+     4.44f, 0.799f, 0.628f, 0.529f, 0.f, 1.99f, 0.069f, 2.38f, 0.67f, 1.24f, 0.f},
+    {kMidTile, kWideCols, kMidStep, 1, 512,
+     6.49f, 1.34f, 1.07f, 0.f, 0.f, 1.69f, 0.062f, 1.87f, 0.59f, 1.03f, 0.f},
 };
-constexpr float kHalfRound = 0.65f;
 constexpr int kMostSplits = 32;          // parts of the k axis
 constexpr int64_t kMostItems = 1 << 24;  // a launch holds fewer than 2^32 threads
 constexpr int64_t kSplitItems = 512;     // a split call fills the chip about once
@@ -689,25 +734,23 @@ static ProductPlan product_plan(const moe_cfg* c, bool dense, int64_t nranks) {
   // segments that may have rows: each costs a block that is not full
   const int64_t live = dense ? 0 : std::min(nranks * (c->E + c->B), best.rows);
   const float out = float(best.rows) * c->Hp / (1 << 20);
+  const float weights = float(live) * c->H * c->Hp / (1 << 20);
   float least = INFINITY;
   for (int k = 0; k < 4; ++k) {
     const Tile& t = kTiles[k];
     const int64_t blocks = (best.rows + t.height - 1) / t.height + live;
-    const int64_t strips = (c->Hp + t.cols - 1) / t.cols, steps = (c->H + t.step - 1) / t.step;
+    const int64_t strips = (c->Hp + t.cols - 1) / t.cols, steps = (c->H + t.step_k - 1) / t.step_k;
     if (blocks * strips >= kMostItems) continue;
     for (int p = 1; p <= kMostSplits; p += p < 4 ? 1 : p < 8 ? 2 : p < 16 ? 4 : 8) {
-      if (p > 1 && (p > steps || blocks * strips * p > kSplitItems * (k < 2 ? 4 : 1))) break;
+      if (p > 1 && (p > steps || blocks * strips * p > kSplitItems * t.waves)) break;
       const int64_t items = blocks * strips * p, n = ((steps + p - 1) / p + t.waves - 1) / t.waves;
-      float rounds = float(items) / t.at_once;
-      if (t.waves == 1) {
-        const int64_t rest = items % t.at_once;
-        rounds = float(items / t.at_once);
-        rounds += rest == 0 ? 0.f : rest <= t.at_once / 2 ? kHalfRound : 1.f;
-      } else if (rounds < 1.f) {
-        rounds = 1.f;
-      }
-      float time = t.start + rounds * (t.steps * n + t.round) + t.filled * n * items / t.at_once;
-      time += t.store * out + (p > 1 ? t.join + t.sums * p * out : 0.f) + (dense ? 0.f : t.list);
+      const int64_t rest = items % t.at_once;
+      const bool half = t.waves == 1 && rest > 0 && rest <= t.at_once / 2;
+      const int64_t rounds = items / t.at_once + (rest > 0 && !half);
+      float time = t.start + rounds * (n * t.step + t.round) + (half ? n * t.half + t.round : 0.f);
+      time += t.filled * n * items / t.at_once + t.store * out;
+      if (p > 1) time += t.join + p * (t.part + t.sums * out);
+      if (!dense) time += t.list + t.weight * weights;
       if (time < least) {
         least = time;
         best.tile = k; best.blocks = int(blocks); best.strips = int(strips);
@@ -816,10 +859,11 @@ extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_
   a.blocks = p.blocks; a.strips = p.strips; a.steps = p.steps; a.splits = p.splits;
   char* at = static_cast<char*>(workspace);
   a.nblocks = reinterpret_cast<int32_t*>(at);
-  a.list = reinterpret_cast<RowItem*>(at + 256);
+  const bool list = plan && nr * segs > kWave * kScan;
+  a.list = list ? reinterpret_cast<RowItem*>(at + 256) : nullptr;
   a.row_expert = reinterpret_cast<int32_t*>(at + expert_at(cfg));
   a.partial = reinterpret_cast<float*>(at + sums_at(cfg));
-  if (plan) hipLaunchKernelGGL(k_row_blocks, dim3(1), dim3(1024), 0, stream, a);
+  if (list) hipLaunchKernelGGL(k_row_blocks, dim3(1), dim3(1024), 0, stream, a);
   if (p.splits == 1) {
     run_product<false>(a, p.tile, stream);
   } else {
