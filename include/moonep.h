@@ -667,8 +667,9 @@ int moe_epilogue_workspace_size(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
  *
  * plan NULL (R = 1 and E = 1): one matrix for all S*K rows -- a shared expert,
  * the router's projection to logits (f32), any dense layer.  w_home [H][Hp];
- * w_pref is not read.  moe_grouped_gemm_dgrad and moe_grouped_gemm_wgrad of the
- * same configuration are its other gradients.
+ * w_pref is not read.  Its other gradients: moe_grouped_gemm_dgrad with
+ * cu_seqlens [0, S*K], and moe_grouped_gemm_wgrad with the same shape in train
+ * mode (B = 1, a slot that nothing uses) and a plan of ids that are all zero.
  *
  * Few rows (decoding) go to a kernel that reads the weights once with every
  * compute unit, in a fixed order of sums: the same call gives the same bits, a
