@@ -52,9 +52,10 @@ __device__ __forceinline__ int segment_of(const int32_t* cu, int n, int row) {
   return wave_sum(before);
 }
 
-// Loads of U rows go out before the first of them is used or stored, so dz may
-// be what is read.  524,288 rows of 2,048 over 384 experts, gelu, bf16: 1.19 ms
-// (5.4 TB/s), 1.27 with dropout; 1.25 and 1.31 through the caches.
+// Blocks of 4 U rows, U a wave: their loads go out first, before the block's
+// segments are known and before any of them is stored, so dz may be what is read.
+// 524,288 rows of 2,048 over 384 experts, gelu, bf16: 1.19 ms (5.4 TB/s), 1.27
+// with dropout; 1.25 and 1.31 through the caches.
 template <typename D, int U>
 __global__ __launch_bounds__(256) void k_eb(EbArgs a) {
   __shared__ f32x4 s_sum[3][2][kWave];
@@ -66,46 +67,25 @@ __global__ __launch_bounds__(256) void k_eb(EbArgs a) {
   for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
     const int chunk = int(w / a.col_tiles), n = int(w % a.col_tiles) * kEbCols + lane * 8;
     const bool on = n < a.N;
-    int64_t row = int64_t(chunk) * a.chunk_rows;
-    const int64_t end = min(row + a.chunk_rows, a.rows);
-    while (row < end) {
-      // [row, stop): the chunk's rows of one segment
-      int64_t stop = end;
-      int seg = 0;
-      if (a.cu) {
-        const int r = int(row / a.SK);
-        const int32_t* cu = a.cu + int64_t(r) * (segs + 1);
-        const int j = segment_of(cu, segs, int(row - int64_t(r) * a.SK));
-        seg = r * (segs + 1) + j;
-        // (always ahead of `row`, whatever cu holds: the loop ends)
-        stop = min(end, max(row + 1, int64_t(r) * a.SK + (j < segs ? cu[j + 1] : a.SK)));
-      }
-      const int rows = int(stop - row);
-      float sum[8];
+    const int64_t from = int64_t(chunk) * a.chunk_rows;
+    const int64_t end = min(from + a.chunk_rows, a.rows);
+    // the segment of row `row` and the row after its last (always ahead of
+    // `row`, whatever cu holds: the loops end)
+    int seg = 0;
+    int64_t stop = end + 1;
+    auto find = [&](int64_t row) {
+      if (!a.cu) return;
+      const int r = int(row / a.SK);
+      const int32_t* cu = a.cu + int64_t(r) * (segs + 1);
+      const int j = segment_of(cu, segs, int(row - int64_t(r) * a.SK));
+      seg = r * (segs + 1) + j;
+      stop = max(row + 1, int64_t(r) * a.SK + (j < segs ? cu[j + 1] : a.SK));
+    };
+    float sum[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-      for (int m0 = on ? wv : rows; m0 < rows; m0 += 4 * U) {
-        float d[U][8], z[U][8];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          // a row past the last is the last again, and is left out below
-          const int64_t at = (row + min(m0 + 4 * u, rows - 1)) * a.N + n;
-          load8_once(static_cast<const D*>(a.dy) + at, d[u]);
-          if (a.act != MOE_ACT_NONE) load8_once(a.pre + at, z[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (m0 + 4 * u >= rows) break;
-          const int64_t at = (row + m0 + 4 * u) * a.N + n;
-          if (a.cut) drop8(d[u], key, uint64_t(at) >> 3, a.cut, a.scale);
-          if (a.act != MOE_ACT_NONE) act_grad8(d[u], z[u], a.act);
-          if (a.dz) store8_once(a.dz + at, d[u]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] += d[u][i];
-        }
-      }
-      row = stop;
-      if (!a.dbias) continue;
+    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    // the waves' sums joined and written; the next segment starts from zero
+    auto flush = [&]() {
       if (wv > 0) {
         s_sum[wv - 1][0][lane] = f32x4{sum[0], sum[1], sum[2], sum[3]};
         s_sum[wv - 1][1][lane] = f32x4{sum[4], sum[5], sum[6], sum[7]};
@@ -124,7 +104,49 @@ __global__ __launch_bounds__(256) void k_eb(EbArgs a) {
         store8(a.part + (int64_t(chunk) + seg) * a.N + n, sum);
       }
       __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    };
+    for (int64_t row = from; row < end; row += 4 * U) {
+      const int have = int(min(int64_t(4 * U), end - row));
+      float d[U][8], z[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[u][i] = z[u][i] = 0.f;
+        // a row past the last is the last again, and is left out below
+        const int64_t at = (row + min(wv + 4 * u, have - 1)) * a.N + n;
+        if (on) {
+          load8_once(static_cast<const D*>(a.dy) + at, d[u]);
+          if (a.act != MOE_ACT_NONE) load8_once(a.pre + at, z[u]);
+        }
+      }
+      if (a.dbias && row == from) find(row);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (wv + 4 * u >= have) break;                    // uniform
+        const int64_t at = (row + wv + 4 * u) * a.N + n;
+        if (a.cut) drop8(d[u], key, uint64_t(at) >> 3, a.cut, a.scale);
+        if (a.act != MOE_ACT_NONE) act_grad8(d[u], z[u], a.act);
+        if (a.dz && on) store8_once(a.dz + at, d[u]);
+      }
+      if (!a.dbias) continue;
+      // the block's rows segment by segment
+      for (int done = 0; done < have;) {
+        const int lim = (int)min(int64_t(have), stop - row);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (wv + 4 * u >= done && wv + 4 * u < lim)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += d[u][i];
+        done = lim;
+        if (row + done == stop) {
+          flush();
+          if (stop < end) find(stop);
+        }
+      }
     }
+    if (a.dbias && stop > end) flush();
   }
 }
 
@@ -258,8 +280,16 @@ extern "C" int moe_epilogue_backward(const moe_cfg* cfg, const moe_epilogue_cfg*
     // (a launch holds fewer than 2^32 threads)
     const dim3 grid((unsigned)std::min<int64_t>(int64_t(a.chunks) * a.col_tiles, 1 << 20)),
         block(256);
-    if (ec->f32) hipLaunchKernelGGL((k_eb<float, 2>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((k_eb<uint16_t, 2>), grid, block, 0, stream, a);
+    // all rows of the smallest chunk at once: its time is the latency of one look
+    // (4,100 rows of 520: 12.5 us by two rows a wave, 9.1 by four); in long chunks
+    // fewer registers pay (1.27 against 1.30 ms)
+    if (a.chunk_rows == 16) {
+      if (ec->f32) hipLaunchKernelGGL((k_eb<float, 4>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((k_eb<uint16_t, 4>), grid, block, 0, stream, a);
+    } else {
+      if (ec->f32) hipLaunchKernelGGL((k_eb<float, 2>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((k_eb<uint16_t, 2>), grid, block, 0, stream, a);
+    }
   } else {
     a.cu = nullptr;                                    // no parts: zeros
   }

@@ -65,12 +65,23 @@ def workspace(c, ec):
 
 
 def products(x, w, expert):
-    """x @ w[expert] by rows in float64, and the sums of the terms' magnitudes."""
-    z, t = np.zeros((x.shape[0], w.shape[2])), np.zeros((x.shape[0], w.shape[2]))
+    """x @ w[expert] by rows in float64, and the sums of the terms' magnitudes (GPU tensors)."""
+    z = torch.zeros((x.shape[0], w.shape[2]), dtype=torch.float64, device="cuda")
+    t = torch.zeros_like(z)
     for e in np.unique(expert[expert >= 0]):
-        at = expert == e
-        z[at], t[at] = x[at] @ w[e], np.abs(x[at]) @ np.abs(w[e])
-    return z, t
+        at = torch.from_numpy(np.nonzero(expert == e)[0]).cuda()
+        xe, we = x.index_select(0, at).double(), w[int(e)].double()
+        z[at], t[at] = xe @ we, xe.abs() @ we.abs()
+    return z.cpu().numpy(), t.cpu().numpy()
+
+
+def some_rows(n, seed, most=700):
+    """All of n rows, or those around the first and last tiles' ends and others at random."""
+    if n <= most:
+        return np.arange(n)
+    near = [b + d for b in (0, 16, 32, 64, 128, 256, n // 2, n // 128 * 128, n) for d in range(-2, 3)]
+    pick = np.random.default_rng(seed).integers(0, n, most - len(near))
+    return np.unique(np.clip(np.concatenate([near, pick]), 0, n - 1))
 
 
 class Case:
@@ -110,19 +121,22 @@ class Case:
         dead = torch.from_numpy(np.nonzero(~live)[0]).cuda()
         self.y.check(dead)
         at = np.nonzero(live)[0]
+        at = at[some_rows(len(at), c.H)]
+        idx = torch.from_numpy(at).cuda()
+        take = lambda t: f64(t.index_select(0, idx))
         e = self.expert[at]
-        z, terms = products(f64(self.x)[at], f64(self.w), e)
+        z, terms = products(self.x.index_select(0, idx), self.w, e)
         if self.bias is not None:
             z = z + f64(self.bias)[e]
             terms = terms + np.abs(f64(self.bias)[e])
         dz = z_tol(c.H, terms)
         f = O.row_factor(self.p, [0, 0] if self.rng is None else self.rng.tolist(), at, c.Hp)
-        res = None if self.residual is None else f64(self.residual)[at]
-        close(f64(self.y.t)[at], O.forward(z, self.kind, self.p, [0, 0] if self.rng is None else self.rng.tolist(),
+        res = None if self.residual is None else take(self.residual)
+        close(take(self.y.t), O.forward(z, self.kind, self.p, [0, 0] if self.rng is None else self.rng.tolist(),
                                            res, at), product_tol(z, dz, self.kind, f, res, self.f32), "y")
         if self.pre is not None:
             self.pre.check(dead)
-            close(f64(self.pre.t)[at], z, (1 + 2.0 ** -8) * dz + round_tol(z, False), "pre")
+            close(take(self.pre.t), z, (1 + 2.0 ** -8) * dz + round_tol(z, False), "pre")
         return self
 
 
@@ -179,6 +193,37 @@ def test_experts(shape, ids, ranks):
         experts(shape, (shape.S + n) % 6, picked, ranks=ranks, seed=10 * n + shape.S, **kw)().check()
 
 
+# Each tile height and width, with the k axis whole and in parts, by the count of segments that
+# every wave does itself (at most 512 of them) and by a list: what the time model picks for these
+# sizes is noted beside them.
+@pytest.mark.parametrize("R,S,E,K,H,Hp,B", [
+    (1, 1, 1, 1, 840, 104, 0), (1, 1, 1, 1, 3016, 16, 0), (1, 13, 1, 1, 7168, 392, 0),    # 16 rows; in 12 and 16 parts
+    (1, 4560, 1, 1, 528, 32, 0), (1, 395, 1, 1, 4208, 16, 0),                 # 32 rows; in 12
+    (1, 556, 1, 1, 376, 3984, 0), (1, 7955, 1, 1, 1520, 16, 0),               # 128 x 128; in 4
+    (1, 1417, 1, 1, 376, 6040, 0), (1, 513, 1, 1, 3976, 6568, 0),             # 128 x 256; in 3
+    (1, 1, 2, 2, 792, 360, 0), (1, 1, 2, 1, 3176, 24, 0),                     # 16 rows; in 16
+    (1, 2144, 16, 2, 528, 32, 0), (1, 155, 4, 2, 6000, 24, 0),                # 32 rows; in 16
+    (1, 57, 8, 2, 368, 6664, 0), (1, 3374, 8, 1, 2128, 24, 0),                # 128 x 128; in 6
+    (4, 225, 64, 2, 632, 744, 16), (1, 332, 24, 2, 5968, 408, 0),             # 128 x 256; in 8
+    (8, 1, 128, 2, 496, 32, 16), (4, 3, 128, 2, 2552, 16, 32),                # by a list: 16 rows; in 12
+    (4, 53, 128, 2, 2928, 64, 32), (4, 5, 128, 2, 2608, 480, 32),             # 32 rows; in 3
+    (4, 293, 128, 2, 40, 176, 32), (4, 39, 128, 2, 408, 6568, 32)])           # 128 x 128; 128 x 256
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
+def test_every_tile(R, S, E, K, H, Hp, B, f32):
+    kind, kw = (S + H // 8) % 6, {"residual": True, "f32": f32, "p": 0.1, "pre": True, "seed": S}
+    if E == 1:
+        matrix(S, H, Hp, kind, **kw)().check()
+        return
+    s = W.TINY.with_(R=R, S=S, E=E, K=K, H=H, Hp=Hp, B=B, mode=0 if B else 1)
+    k = experts(s, kind, W.routing_uniform(s, 6)[0], **kw)()
+    k.check()
+    y = k.y.t.clone()
+    k.ws.fill_(0x11)                                       # nothing in the workspace matters
+    k()
+    i = torch.int32 if f32 else torch.int16
+    assert torch.equal(y.view(i), k.y.t.view(i))
+
+
 def test_failed_plan_writes_nothing():
     for S in (16, 400):
         s = W.TINY.with_(S=S)
@@ -212,10 +257,11 @@ def test_in_place_and_repeatable(S):
     assert torch.equal(y.view(torch.int16), buf.view(torch.int16))
 
 
-@pytest.mark.parametrize("S", [4, 100, 1400])
-def test_rows_and_columns_are_apart(S):
+# k ends inside a step, columns inside a strip; every tile shape, and parts of the k axis
+@pytest.mark.parametrize("S,H,Hp", [(4, 136, 152), (100, 136, 152), (1400, 136, 152), (13, 7144, 392),
+                                    (556, 376, 3984), (7955, 1528, 16), (1417, 376, 6040), (513, 3976, 6568)])
+def test_rows_and_columns_are_apart(S, H, Hp):
     """Infinities and NaN stay in the rows and columns whose definition has them."""
-    H, Hp = 136, 152                                      # k ends inside a step, columns inside a strip
     k = matrix(S, H, Hp, O.NONE, residual=True, p=0.0, seed=6)()
     clean = k.y.t.clone()
     k.x[S // 2] = float("nan")
@@ -231,21 +277,23 @@ def test_rows_and_columns_are_apart(S):
     assert torch.isnan(k.y.t[:, Hp - 1]).all() and torch.isnan(k.y.t[S // 2]).all()
 
 
-def test_neighbours_do_not_leak():
+@pytest.mark.parametrize("shape", [W.TINY.with_(H=136, Hp=72), W.TINY.with_(S=300, H=136, Hp=72),
+                                   W.TINY.with_(R=4, S=225, E=64, K=2, H=632, Hp=744, B=16),
+                                   W.TINY.with_(R=4, S=293, E=128, K=2, H=40, Hp=176, B=32)], ids=str)
+def test_neighbours_do_not_leak(shape):
     """Rows of other segments and weights of other experts are NaN; one segment is clean."""
-    for S in (16, 300):
-        k = experts(W.TINY.with_(S=S, H=136, Hp=72), O.GELU, W.routing_uniform(W.TINY.with_(S=S), 5)[0], seed=7)()
-        clean = k.y.t.clone()
-        e = int(np.bincount(k.expert[k.expert >= 0]).argmax())
-        keep = torch.from_numpy(k.expert == e).cuda()
-        k.x[~keep] = float("nan")
-        k.bias[torch.arange(8, device="cuda") != e] = float("nan")
-        for j in range(8):
-            if j != e:
-                k.w[j] = float("nan")
-        mx.moe_prefetch_weight(k.c, k.plan, k.w, k.w_pref)
-        k()
-        assert torch.equal(k.y.t[keep].view(torch.int16), clean[keep].view(torch.int16))
+    k = experts(shape, O.GELU, W.routing_uniform(shape, 5)[0], seed=7)()
+    clean = k.y.t.clone()
+    e = int(np.bincount(k.expert[k.expert >= 0]).argmax())
+    keep = torch.from_numpy(k.expert == e).cuda()
+    others = torch.arange(shape.E, device="cuda") != e
+    k.x[~keep] = float("nan")
+    k.bias[others] = float("nan")
+    k.w[others] = float("nan")
+    mx.moe_prefetch_weight(k.c, k.plan, k.w, k.w_pref)
+    k()
+    assert torch.equal(k.y.t[keep].view(torch.int16), clean[keep].view(torch.int16))
+    assert torch.isnan(k.y.t[~keep]).all()
 
 
 def test_special_values_of_the_activations():
@@ -445,9 +493,8 @@ def test_many_rows():
     at = np.concatenate([np.arange(5), np.arange(per - 3, per + 3), np.arange(mid - 3, mid + 3),
                          np.arange(rows - 5, rows)])
     idx = torch.from_numpy(at).cuda()
-    xs = f64(x.index_select(0, idx))
     e = at // per
-    z, t = products(xs, f64(w), e)
+    z, t = products(x.index_select(0, idx), w, e)
     z, t = z + f64(bias)[e], t + np.abs(f64(bias)[e])
     dz = z_tol(H, t)
     f = O.row_factor(0.5, [9, 9], at, Hp)
