@@ -40,6 +40,7 @@ struct ProductArgs {
   int32_t H, E, B, SK, first_rank, nranks;
   int32_t rows, height, cols, strips, steps, splits;
   int32_t blocks;            // grouped: the most there may be
+  int32_t once;              // about one block for each segment, weights not in the caches
   Epilogue ep;
 };
 
@@ -119,7 +120,10 @@ __device__ __forceinline__ bool my_block(const ProductArgs& a, RowBlock& b) {
   const int place = blockIdx.x / 8, item = (blockIdx.x % 8) * share + place;
   if (place >= share || item >= items) return false;
   b.split = item / units;
-  const int u = item % units, near = u / a.strips;         // a block of the same segment
+  int u = item % units;
+  // few rows of many experts: strip by strip over the experts, not expert by expert
+  if (a.once) u = u % blocks * a.strips + u / blocks;
+  const int near = u / a.strips;                           // a block of the same segment
   int first = 0, cnt = blocks, seg = 0;
   if (scan) {
 #pragma unroll
@@ -207,8 +211,15 @@ __device__ __forceinline__ void column_pair(const u32x4 (&w)[8], int j, bf16x8& 
   odd = __builtin_bit_cast(bf16x8, o);
 }
 
-// RB: blocks of 16 rows that a workgroup takes.
-template <int RB, bool SPLIT>
+// RB: blocks of 16 rows that a workgroup takes.  ONCE: weights that are too many
+// for the caches, and read by about one block each, pass them by, and strips are
+// taken over the experts in turn (my_block).  One token on each of 8 ranks, 41
+// experts of 7,168 x 2,048 met: 224 us through the caches expert by expert, 209
+// strip by strip, 201 past them, 189 both (6.3 TB/s).  Not so where blocks share
+// weights (568 rows over 60 experts of 880 x 6,576: 116, 154, 133, 171) or where
+// the last cache holds them from call to call (64 experts of 1,024 x 512: 10, 10,
+// 13, 12).
+template <int RB, bool SPLIT, bool ONCE>
 __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
   __shared__ f32x4 s_sum[4 * 3 * RB * kWave * 2];
   RowBlock rb;
@@ -239,8 +250,10 @@ __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
     const bool in = k < H;
     const uint32_t wk = wcol + 2u * uint32_t(in ? k : 0) * N;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      wr[q] = *reinterpret_cast<const u32x4*>(w + (wk + 2u * uint32_t(q) * N));
+    for (int q = 0; q < 8; ++q) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(w + (wk + 2u * uint32_t(q) * N));
+      wr[q] = ONCE ? __builtin_nontemporal_load(p) : *p;
+    }
 #pragma unroll
     for (int b = 0; b < RB; ++b)
       xr[b] = *reinterpret_cast<const u32x4*>(x + (xrow[b] + 2u * uint32_t(in ? k : 0)));
@@ -700,32 +713,35 @@ __global__ __launch_bounds__(256) void k_join(ProductArgs a) {
 // (tiles in LDS; the others count it whole), and
 //   + join + parts * part + parts * outputs / 2^20 * sums    if k is cut into parts,
 //   + list + weights of the segments with rows / 2^20 * weight    for experts.
-// Fitted (non-negative least squares of the relative error) to 8,011 timings of
-// 406 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
-// 7,168, one to 384 experts.  The median error is 4 %; what the model picks was
-// 1.7 % slower than the best of them on average, 25 % at worst.
+// Fitted (non-negative least squares of the relative error) to 7,595 timings of
+// 416 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
+// 7,168, one to 384 experts.  The median error is 4 to 5 %; what the model picks
+// was 1.4 % slower than the best of them on average, 32 % at worst.
 struct Tile {
   int height, cols, step_k, waves, at_once;
   float start, step, half, round, filled, join, part, sums, store, list, weight;
 };
 constexpr Tile kTiles[4] = {
     {16, kFewCols, kFewStep, 4, 768,
-     3.80f, 0.402f, 0.f, 0.643f, 0.803f, 2.14f, 0.065f, 2.34f, 0.89f, 1.06f, 0.036f},
+     3.93f, 0.413f, 0.f, 0.55f, 0.801f, 1.99f, 0.084f, 2.37f, 0.877f, 1.05f, 0.069f},
     {32, kFewCols, kFewStep, 4, 512,
-     3.77f, 0.429f, 0.f, 1.12f, 0.564f, 2.09f, 0.062f, 2.03f, 0.89f, 1.10f, 0.018f},
+     3.92f, 0.437f, 0.f, 1.01f, 0.577f, 1.90f, 0.086f, 2.02f, 0.889f, 1.11f, 0.045f},
     {kMidTile, kMidTile, kMidStep, 1, 512,
-     4.44f, 0.799f, 0.628f, 0.529f, 0.f, 1.99f, 0.069f, 2.38f, 0.67f, 1.24f, 0.f},
+     5.08f, 0.824f, 0.629f, 0.f, 0.f, 1.83f, 0.087f, 2.33f, 0.72f, 1.22f, 0.f},
     {kMidTile, kWideCols, kMidStep, 1, 512,
-     6.49f, 1.34f, 1.07f, 0.f, 0.f, 1.69f, 0.062f, 1.87f, 0.59f, 1.03f, 0.f},
+     6.43f, 1.37f, 1.06f, 0.f, 0.f, 1.71f, 0.081f, 1.86f, 0.603f, 0.982f, 0.f},
 };
 constexpr int kMostSplits = 32;          // parts of the k axis
 constexpr int64_t kMostItems = 1 << 24;  // a launch holds fewer than 2^32 threads
 constexpr int64_t kSplitItems = 512;     // a split call fills the chip about once
+constexpr int64_t kCached = 256 << 20;   // bytes that the last cache holds
+constexpr int64_t kOnceRows = 4;         // mean rows of a segment that is about one block
 
 // Everything that the host decides about a call, from its configuration alone.
 struct ProductPlan {
   int64_t rows;
   int tile, blocks, strips, steps, splits;
+  bool once;      // the weights are not in the caches, and are read by one block each
 };
 
 static ProductPlan product_plan(const moe_cfg* c, bool dense, int64_t nranks) {
@@ -758,6 +774,8 @@ static ProductPlan product_plan(const moe_cfg* c, bool dense, int64_t nranks) {
       }
     }
   }
+  best.once = best.tile < 2 && !dense && int64_t(c->E) * c->H * c->Hp * 2 > kCached &&
+              best.rows <= kOnceRows * live;
   return best;
 }
 
@@ -784,11 +802,13 @@ static size_t epilogue_ws_bytes(const moe_cfg* c) {
 }
 
 template <bool SPLIT>
-static void run_product(const ProductArgs& a, int tile, hipStream_t stream) {
+static void run_product(const ProductArgs& a, int tile, bool once, hipStream_t stream) {
   const int64_t items = int64_t(a.blocks) * a.strips * a.splits;
   const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(256);
-  if (tile == 0) hipLaunchKernelGGL((k_few<1, SPLIT>), grid, block, 0, stream, a);
-  else if (tile == 1) hipLaunchKernelGGL((k_few<2, SPLIT>), grid, block, 0, stream, a);
+  if (tile == 0 && once) hipLaunchKernelGGL((k_few<1, SPLIT, true>), grid, block, 0, stream, a);
+  else if (tile == 0) hipLaunchKernelGGL((k_few<1, SPLIT, false>), grid, block, 0, stream, a);
+  else if (tile == 1 && once) hipLaunchKernelGGL((k_few<2, SPLIT, true>), grid, block, 0, stream, a);
+  else if (tile == 1) hipLaunchKernelGGL((k_few<2, SPLIT, false>), grid, block, 0, stream, a);
   else if (tile == 2) hipLaunchKernelGGL((k_mid<SPLIT>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((k_wide<SPLIT>), grid, block, 0, stream, a);
 }
@@ -856,7 +876,7 @@ extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_
   a.H = cfg->H; a.E = cfg->E; a.B = cfg->B; a.SK = (int32_t)SK;
   a.first_rank = rank_begin; a.nranks = (int32_t)nr; a.rows = (int32_t)p.rows;
   a.height = kTiles[p.tile].height; a.cols = kTiles[p.tile].cols;
-  a.blocks = p.blocks; a.strips = p.strips; a.steps = p.steps; a.splits = p.splits;
+  a.once = p.once; a.blocks = p.blocks; a.strips = p.strips; a.steps = p.steps; a.splits = p.splits;
   char* at = static_cast<char*>(workspace);
   a.nblocks = reinterpret_cast<int32_t*>(at);
   const bool list = plan && nr * segs > kWave * kScan;
@@ -865,9 +885,9 @@ extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_
   a.partial = reinterpret_cast<float*>(at + sums_at(cfg));
   if (list) hipLaunchKernelGGL(k_row_blocks, dim3(1), dim3(1024), 0, stream, a);
   if (p.splits == 1) {
-    run_product<false>(a, p.tile, stream);
+    run_product<false>(a, p.tile, p.once, stream);
   } else {
-    run_product<true>(a, p.tile, stream);
+    run_product<true>(a, p.tile, p.once, stream);
     const int64_t groups = p.rows * (cfg->Hp / 8);
     hipLaunchKernelGGL(k_join, dim3((unsigned)((groups + 255) / 256)), dim3(256), 0, stream, a);
   }

@@ -198,11 +198,13 @@ def test_experts(shape, ids, ranks):
 # sizes is noted beside them.
 @pytest.mark.parametrize("R,S,E,K,H,Hp,B", [
     (1, 1, 1, 1, 840, 104, 0), (1, 1, 1, 1, 3016, 16, 0), (1, 13, 1, 1, 7168, 392, 0),    # 16 rows; in 12 and 16 parts
-    (1, 4560, 1, 1, 528, 32, 0), (1, 395, 1, 1, 4208, 16, 0),                 # 32 rows; in 12
+    (1, 4560, 1, 1, 528, 32, 0), (1, 998, 1, 1, 2064, 16, 0),                 # 32 rows; in 6
     (1, 556, 1, 1, 376, 3984, 0), (1, 7955, 1, 1, 1520, 16, 0),               # 128 x 128; in 4
     (1, 1417, 1, 1, 376, 6040, 0), (1, 513, 1, 1, 3976, 6568, 0),             # 128 x 256; in 3
     (1, 1, 2, 2, 792, 360, 0), (1, 1, 2, 1, 3176, 24, 0),                     # 16 rows; in 16
-    (1, 2144, 16, 2, 528, 32, 0), (1, 155, 4, 2, 6000, 24, 0),                # 32 rows; in 16
+    (1, 2144, 16, 2, 528, 32, 0), (1, 20, 16, 1, 1960, 824, 0),               # 32 rows; in 4
+    (1, 2, 24, 2, 1200, 4832, 0), (1, 1, 24, 1, 1000, 5608, 0),               # 16 rows past the caches; in 8
+    (1, 1, 24, 8, 1008, 5640, 0), (1, 1, 24, 8, 2648, 2160, 0),               # 32 rows past the caches; in 3
     (1, 57, 8, 2, 368, 6664, 0), (1, 3374, 8, 1, 2128, 24, 0),                # 128 x 128; in 6
     (4, 225, 64, 2, 632, 744, 16), (1, 332, 24, 2, 5968, 408, 0),             # 128 x 256; in 8
     (8, 1, 128, 2, 496, 32, 16), (4, 3, 128, 2, 2552, 16, 32),                # by a list: 16 rows; in 12
