@@ -271,8 +271,9 @@ __device__ __forceinline__ void epilogue8(const Epilogue& ep, const DropKey& key
 // A wave's block of z staged in LDS: groups 0 .. 7 of this lane, group k at
 // place(k, at) (its eight values; `at` the flat index of the first in y), null
 // where there is none.  All residuals are asked for before the first group's
-// arithmetic, which is a loop of its own (the activations are long code) and
-// leaves its values where they were; the last loop only adds and stores.
+// arithmetic.  The activations are long code: a loop of their own, which leaves
+// the values where they were.  Without one a group goes through in one piece
+// (8,192 x 2,048 x 7,168 with dropout and residual: 264 us by two loops, 251).
 template <typename Place>
 __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey& key,
                                                Place&& place) {
@@ -283,7 +284,8 @@ __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey
       int64_t at = 0;
       if (place(k, at)) r[k] = residual8(ep, at);
     }
-  if (ep.pre || ep.cut || ep.act != MOE_ACT_NONE)
+  const bool plain = ep.act == MOE_ACT_NONE;
+  if (!plain)
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
       int64_t at = 0;
@@ -301,6 +303,8 @@ __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey
     if (!p) continue;
     float z[8];
     load8(p, z);
+    if (plain && ep.pre) store8_once(ep.pre + at, z);
+    if (plain && ep.cut) drop8(z, key, uint64_t(at) >> 3, ep.cut, ep.scale);
     finish8(ep, z, r[k], at);
   }
 }
