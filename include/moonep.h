@@ -632,7 +632,7 @@ enum {
  * (low and high half of rng[0]); value i % 8 = 2w or 2w + 1 takes the low or
  * high half of word w.  rng [2] int64 on the device: the seed, and a number that
  * the caller changes from use to use (the step, say), so a captured graph draws
- * new numbers when the caller writes new ones there.  A backward given the same
+ * new numbers when the caller writes new ones there; an 8-byte boundary.  A backward given the same
  * rng contents and the same p drops the same values; no mask is stored.
  */
 
@@ -676,8 +676,10 @@ int moe_epilogue_workspace_size(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
  * call with other rows beside them need not.  y may be residual (in place);
  * apart from that the listed ranks' rows of y and pre and the workspace
  * (moe_epilogue_workspace_size() bytes; concurrent calls need distinct ones)
- * must not overlap each other or the inputs.  MOE_ELIMIT from 2^24 tiles of 128
- * rows and 256 columns on (every segment's last tile counted whole).
+ * must not overlap each other or the inputs.  NaN and infinities pass through the
+ * sums and functions that they enter as IEEE arithmetic has it.  MOE_ELIMIT from
+ * 2^24 - 8 tiles of 128 rows and 256 columns on (each segment's last counted
+ * whole).
  */
 int moe_grouped_gemm_epilogue(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
                               const moe_plan *plan, const moe_bf16 *xperm,

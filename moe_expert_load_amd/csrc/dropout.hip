@@ -238,7 +238,7 @@ extern "C" int moe_dropout(const moe_dropout_cfg* dc, int64_t rows, int32_t widt
   if (rows < 0 || width < 8 || width % 8 != 0) return MOE_EINVAL;
   if (rows > ((int64_t(1) << 40) - 1) / width) return MOE_ELIMIT;
   if (rows == 0) return MOE_OK;
-  if (!src || !dst || (cut && !rng) || !aligned16(src, residual, dst)) return MOE_EINVAL;
+  if (!src || !dst || !rng_ok(rng, cut) || !aligned16(src, residual, dst)) return MOE_EINVAL;
   const int64_t bytes = rows * width * (dc->f32 ? 4 : 2);
   if (clash({{dst, bytes}}, {{dst == src ? nullptr : src, bytes},
                              {dst == residual ? nullptr : residual, bytes},
@@ -261,7 +261,7 @@ extern "C" int moe_combine_dropout(const moe_cfg* cfg, const moe_dropout_cfg* dc
   if (!valid_dropout(dc, &cut, &scale)) return MOE_EINVAL;
   const int64_t ntok = int64_t(cfg->R) * cfg->S, rows = ntok * cfg->K;
   if (ntok == 0) return MOE_OK;
-  if (!plan || !plan->route || !y || !gates || !out || (cut && !rng)) return MOE_EINVAL;
+  if (!plan || !plan->route || !y || !gates || !out || !rng_ok(rng, cut)) return MOE_EINVAL;
   if (!aligned16(y, residual, out)) return MOE_EINVAL;
   const int64_t bytes = ntok * cfg->Hp * (dc->f32 ? 4 : 2);
   if (clash({{out, bytes}}, {{y, rows * cfg->Hp * 2},
@@ -298,7 +298,7 @@ extern "C" int moe_combine_dropout_backward(const moe_cfg* cfg, const moe_dropou
   if (!valid_dropout(dc, &cut, &scale)) return MOE_EINVAL;
   const int64_t ntok = int64_t(cfg->R) * cfg->S, rows = ntok * cfg->K;
   if (ntok == 0) return MOE_OK;
-  if (!plan || !plan->route || !dout || !y || !gates || !dy || !dgates || (cut && !rng))
+  if (!plan || !plan->route || !dout || !y || !gates || !dy || !dgates || !rng_ok(rng, cut))
     return MOE_EINVAL;
   if (!aligned16(dout, y, dy)) return MOE_EINVAL;
   if (clash({{dy, rows * cfg->Hp * 2}, {dgates, rows * 4}},

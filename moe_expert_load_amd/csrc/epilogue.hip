@@ -250,7 +250,7 @@ extern "C" int moe_epilogue_backward(const moe_cfg* cfg, const moe_epilogue_cfg*
   EbArgs a{};
   drop_params(ec->p, &a.cut, &a.scale);
   if (rows > 0) {
-    if (!dy || (a.cut && !rng) || (ec->act != MOE_ACT_NONE && !pre)) return MOE_EINVAL;
+    if (!dy || !rng_ok(rng, a.cut) || (ec->act != MOE_ACT_NONE && !pre)) return MOE_EINVAL;
   }
   if (dbias && !workspace) return MOE_EINVAL;
   if (dbias && plan && (!plan->cu_seqlens || (cfg->B > 0 && !plan->slot_expert))) return MOE_EINVAL;

@@ -340,6 +340,11 @@ inline bool drop_params(float p, uint32_t* cut, float* scale) {
   return true;
 }
 
+// Whether rng can be read as two int64, or is not needed.
+inline bool rng_ok(const int64_t* rng, uint32_t cut) {
+  return cut == 0 || (rng && (reinterpret_cast<uintptr_t>(rng) & 7) == 0);
+}
+
 inline bool valid_epilogue(const moe_epilogue_cfg* ec) {
   uint32_t cut;
   float scale;

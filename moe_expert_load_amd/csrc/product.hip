@@ -732,7 +732,7 @@ constexpr Tile kTiles[4] = {
      6.43f, 1.37f, 1.06f, 0.f, 0.f, 1.71f, 0.081f, 1.86f, 0.603f, 0.982f, 0.f},
 };
 constexpr int kMostSplits = 32;          // parts of the k axis
-constexpr int64_t kMostItems = 1 << 24;  // a launch holds fewer than 2^32 threads
+constexpr int64_t kMostItems = (1 << 24) - 8;  // a launch holds fewer than 2^32 threads
 constexpr int64_t kSplitItems = 512;     // a split call fills the chip about once
 constexpr int64_t kCached = 256 << 20;   // bytes that the last cache holds
 constexpr int64_t kOnceRows = 4;         // mean rows of a segment that is about one block
@@ -843,7 +843,7 @@ extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_
   Epilogue& ep = a.ep;
   drop_params(ec->p, &ep.cut, &ep.scale);
   const bool slots = plan && cfg->B > 0;
-  if (!xperm || !w_home || !y || !workspace || (ep.cut && !rng)) return MOE_EINVAL;
+  if (!xperm || !w_home || !y || !workspace || !rng_ok(rng, ep.cut)) return MOE_EINVAL;
   if (plan && !plan->cu_seqlens) return MOE_EINVAL;
   if (slots && (!w_pref || !plan->slot_expert)) return MOE_EINVAL;
   if (!aligned16(xperm, w_home, slots ? w_pref : nullptr, bias, residual, y, pre, workspace))

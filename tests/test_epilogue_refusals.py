@@ -100,6 +100,22 @@ def test_product_overlaps(lib):
     assert product(lib, plan=plan) == E
 
 
+def test_rng_boundary(lib):
+    """Two int64 on their own boundary, wherever something is dropped."""
+    odd = at((40 << 34) + 4)
+    dc, c, p = ref(mx.make_dropout_cfg(0.1)), ref(CFG), ref(PLAN)
+    assert product(lib, rng=odd) == E and backward(lib, rng=odd) == E
+    assert lib.moe_dropout(dc, 4, 64, far(1), far(2), odd, far(4), None) == E
+    assert lib.moe_combine_dropout(c, dc, p, far(1), far(2), far(3), odd, far(5), None) == E
+    assert lib.moe_combine_dropout_backward(c, dc, p, far(1), far(2), far(3), odd, far(5), far(6), None) == E
+
+
+def test_too_many_tiles(lib):
+    big = mx.make_cfg(1024, 16383, 2048, 64, 8, 2040, 0, mx.MODE_INFER)   # 2^30 rows, 8 tiles wide
+    wide = {n: ctypes.c_void_p((i + 1) << 46) for i, n in enumerate(NAMES)}
+    assert product(lib, cfg=big, re=1024, ws=ctypes.c_void_p(20 << 46), **wide) == L
+
+
 def test_one_matrix_arguments(lib):
     assert product(lib, cfg=ONE, plan=None, re=1, y=None) == E
     assert product(lib, cfg=ONE, plan=None, re=1, x=at((1 << 34) + 4)) == E
