@@ -280,17 +280,22 @@ __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
       }
     }
   };
-  // two steps in flight
-  u32x4 w0[8], w1[8], x0[RB], x1[RB];
+  // three steps ahead, four buffers (one token, 7,168 x 2,048 cold: 14.0 us with one
+  // step ahead, 13.3)
+  u32x4 wr[4][8], xr[4][RB];
   int t = t0 + wv;
-  if (t < t1) load(t, w0, x0);
+#pragma unroll
+  for (int u = 0; u < 3; ++u)
+    if (t + 4 * u < t1) load(t + 4 * u, wr[u], xr[u]);
 #pragma unroll 1
-  for (; t < t1; t += 8) {
-    if (t + 4 < t1) load(t + 4, w1, x1);
-    multiply(t, w0, x0);
-    if (t + 4 >= t1) break;
-    if (t + 8 < t1) load(t + 8, w0, x0);
-    multiply(t + 4, w1, x1);
+  for (; t < t1; t += 16) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int now = t + 4 * u, ahead = now + 12;
+      if (now >= t1) break;
+      if (ahead < t1) load(ahead, wr[(u + 3) & 3], xr[(u + 3) & 3]);
+      multiply(now, wr[u], xr[u]);
+    }
   }
 
   // Register v of an accumulator is row 4 (l / 16) + v of its block: wave v
@@ -672,9 +677,10 @@ __global__ __launch_bounds__(256, 2) void k_wide(ProductArgs a) {
     a.row_expert[rb.row0 - first + wm * 64 + lane] = e;
 }
 
-// Sums of the splits in ascending order, and the epilogue.
-__global__ __launch_bounds__(256) void k_join(ProductArgs a) {
-  const int64_t nv = a.ep.N / 8, g = int64_t(blockIdx.x) * 256 + threadIdx.x;
+// Sums of the splits in ascending order, and the epilogue.  Workgroups of one
+// wave: a token's few outputs are spread over the units (14.6 -> 14.0 us there).
+__global__ __launch_bounds__(64) void k_join(ProductArgs a) {
+  const int64_t nv = a.ep.N / 8, g = int64_t(blockIdx.x) * 64 + threadIdx.x;
   if (g >= nv * a.rows) return;
   const int64_t at = g / nv;
   const int n = int(g % nv) * 8;
@@ -713,23 +719,23 @@ __global__ __launch_bounds__(256) void k_join(ProductArgs a) {
 // (tiles in LDS; the others count it whole), and
 //   + join + parts * part + parts * outputs / 2^20 * sums    if k is cut into parts,
 //   + list + weights of the segments with rows / 2^20 * weight    for experts.
-// Fitted (non-negative least squares of the relative error) to 7,595 timings of
+// Fitted (non-negative least squares of the relative error) to 8,384 timings of
 // 416 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
-// 7,168, one to 384 experts.  The median error is 4 to 5 %; what the model picks
-// was 1.4 % slower than the best of them on average, 32 % at worst.
+// 7,168, one to 384 experts.  The median error is 3 to 5 %; what the model picks
+// was 1.9 % slower than the best of them on average, 38 % at worst.
 struct Tile {
   int height, cols, step_k, waves, at_once;
   float start, step, half, round, filled, join, part, sums, store, list, weight;
 };
 constexpr Tile kTiles[4] = {
-    {16, kFewCols, kFewStep, 4, 768,
-     3.93f, 0.413f, 0.f, 0.55f, 0.801f, 1.99f, 0.084f, 2.37f, 0.877f, 1.05f, 0.069f},
+    {16, kFewCols, kFewStep, 4, 512,
+     3.80f, 0.284f, 0.f, 0.678f, 0.491f, 1.77f, 0.070f, 2.64f, 1.09f, 1.11f, 0.027f},
     {32, kFewCols, kFewStep, 4, 512,
-     3.92f, 0.437f, 0.f, 1.01f, 0.577f, 1.90f, 0.086f, 2.02f, 0.889f, 1.11f, 0.045f},
+     4.19f, 0.335f, 0.f, 0.737f, 0.630f, 1.73f, 0.069f, 2.28f, 0.767f, 1.04f, 0.001f},
     {kMidTile, kMidTile, kMidStep, 1, 512,
-     5.08f, 0.824f, 0.629f, 0.f, 0.f, 1.83f, 0.087f, 2.33f, 0.72f, 1.22f, 0.f},
+     5.06f, 0.738f, 0.620f, 0.f, 0.f, 1.77f, 0.073f, 2.50f, 0.696f, 1.30f, 0.f},
     {kMidTile, kWideCols, kMidStep, 1, 512,
-     6.43f, 1.37f, 1.06f, 0.f, 0.f, 1.71f, 0.081f, 1.86f, 0.603f, 0.982f, 0.f},
+     6.43f, 1.31f, 1.07f, 0.f, 0.f, 1.55f, 0.077f, 2.02f, 0.574f, 1.05f, 0.f},
 };
 constexpr int kMostSplits = 32;          // parts of the k axis
 constexpr int64_t kMostItems = (1 << 24) - 8;  // a launch holds fewer than 2^32 threads
@@ -889,7 +895,7 @@ extern "C" int moe_grouped_gemm_epilogue(const moe_cfg* cfg, const moe_epilogue_
   } else {
     run_product<true>(a, p.tile, p.once, stream);
     const int64_t groups = p.rows * (cfg->Hp / 8);
-    hipLaunchKernelGGL(k_join, dim3((unsigned)((groups + 255) / 256)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(k_join, dim3((unsigned)((groups + 63) / 64)), dim3(64), 0, stream, a);
   }
   return hip_status();
 }

@@ -195,21 +195,22 @@ def test_experts(shape, ids, ranks):
 
 # Each tile height and width, with the k axis whole and in parts, by the count of segments that
 # every wave does itself (at most 512 of them) and by a list: what the time model picks for these
-# sizes is noted beside them.
+# sizes, by a margin where it can, is noted beside them.
 @pytest.mark.parametrize("R,S,E,K,H,Hp,B", [
-    (1, 1, 1, 1, 840, 104, 0), (1, 1, 1, 1, 3016, 16, 0), (1, 13, 1, 1, 7168, 392, 0),    # 16 rows; in 12 and 16 parts
-    (1, 4560, 1, 1, 528, 32, 0), (1, 998, 1, 1, 2064, 16, 0),                 # 32 rows; in 6
-    (1, 556, 1, 1, 376, 3984, 0), (1, 7955, 1, 1, 1520, 16, 0),               # 128 x 128; in 4
-    (1, 1417, 1, 1, 376, 6040, 0), (1, 513, 1, 1, 3976, 6568, 0),             # 128 x 256; in 3
+    (1, 2, 1, 1, 728, 24, 0), (1, 1, 1, 1, 5136, 6072, 0), (1, 13, 1, 1, 7160, 392, 0),   # 16 rows; in 6 and 12 parts
+    (1, 943, 1, 1, 360, 1080, 0), (1, 567, 1, 1, 3376, 536, 0),               # 32 rows; in 3
+    (1, 2406, 1, 1, 432, 824, 0), (1, 1485, 1, 1, 3824, 1392, 0),             # 128 x 128; in 3
+    (1, 6881, 1, 1, 360, 7016, 0), (1, 653, 1, 1, 7064, 5520, 0),             # 128 x 256; in 3
     (1, 1, 2, 2, 792, 360, 0), (1, 1, 2, 1, 3176, 24, 0),                     # 16 rows; in 16
-    (1, 2144, 16, 2, 528, 32, 0), (1, 20, 16, 1, 1960, 824, 0),               # 32 rows; in 4
-    (1, 2, 24, 2, 1200, 4832, 0), (1, 1, 24, 1, 1000, 5608, 0),               # 16 rows past the caches; in 8
-    (1, 1, 24, 8, 1008, 5640, 0), (1, 1, 24, 8, 2648, 2160, 0),               # 32 rows past the caches; in 3
-    (1, 57, 8, 2, 368, 6664, 0), (1, 3374, 8, 1, 2128, 24, 0),                # 128 x 128; in 6
-    (4, 225, 64, 2, 632, 744, 16), (1, 332, 24, 2, 5968, 408, 0),             # 128 x 256; in 8
-    (8, 1, 128, 2, 496, 32, 16), (4, 3, 128, 2, 2552, 16, 32),                # by a list: 16 rows; in 12
-    (4, 53, 128, 2, 2928, 64, 32), (4, 5, 128, 2, 2608, 480, 32),             # 32 rows; in 3
-    (4, 293, 128, 2, 40, 176, 32), (4, 39, 128, 2, 408, 6568, 32)])           # 128 x 128; 128 x 256
+    (1, 2, 24, 2, 1200, 4832, 0), (1, 1, 24, 8, 2648, 2160, 0),               # 16 rows past the caches; in 3
+    (1, 1283, 2, 1, 440, 832, 0), (1, 664, 2, 1, 4072, 432, 0),               # 32 rows; in 4
+    (1, 37, 16, 1, 2440, 3496, 0), (1, 18, 16, 2, 5072, 1680, 0),             # 32 rows past the caches; in 2
+    (1, 944, 2, 2, 432, 1312, 0), (1, 562, 2, 2, 3064, 1808, 0),              # 128 x 128; in 3
+    (1, 3570, 2, 2, 376, 6352, 0), (1, 905, 2, 1, 6424, 3248, 0),             # 128 x 256; in 3
+    (8, 1, 128, 2, 496, 32, 16), (4, 67, 128, 2, 2296, 16, 32),               # by a list: 16 rows; in 3
+    (4, 31, 128, 2, 2120, 152, 32), (4, 5, 128, 2, 856, 1424, 32),            # 32 rows; past the caches
+    (4, 5, 128, 2, 2608, 480, 32), (4, 293, 128, 2, 40, 176, 32),             # 32 rows in 3; 128 x 128
+    (4, 39, 128, 2, 408, 6568, 32)])                                          # 128 x 256
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
 def test_every_tile(R, S, E, K, H, Hp, B, f32):
     kind, kw = (S + H // 8) % 6, {"residual": True, "f32": f32, "p": 0.1, "pre": True, "seed": S}
@@ -261,7 +262,8 @@ def test_in_place_and_repeatable(S):
 
 # k ends inside a step, columns inside a strip; every tile shape, and parts of the k axis
 @pytest.mark.parametrize("S,H,Hp", [(4, 136, 152), (100, 136, 152), (1400, 136, 152), (13, 7144, 392),
-                                    (556, 376, 3984), (7955, 1528, 16), (1417, 376, 6040), (513, 3976, 6568)])
+                                    (943, 360, 1080), (567, 3376, 536), (2406, 424, 824), (1485, 3832, 1392),
+                                    (6881, 360, 7016), (653, 7064, 5520)])
 def test_rows_and_columns_are_apart(S, H, Hp):
     """Infinities and NaN stay in the rows and columns whose definition has them."""
     k = matrix(S, H, Hp, O.NONE, residual=True, p=0.0, seed=6)()
