@@ -3,6 +3,7 @@
 // (epilogue.hpp); nothing is stored between the passes.  All three are bound by
 // memory: every tensor is read or written once.
 #include <algorithm>
+#include <type_traits>
 
 #include "epilogue.hpp"
 #include "host.hpp"
@@ -43,26 +44,32 @@ __global__ __launch_bounds__(256) void k_dropout(const T* src, const T* residual
 }
 
 // ---------------------------------------------------------------------------
-// out[t] = residual[t] + dropout(sum_k gates[t][k] * y[route_k]): a wave per
+// out[t] = residual[t] + dropout(sum_k gates[t][k] * y[route_k]): W waves per
 // token, CU groups of eight columns a lane, KB rows in flight (as k_combine).
-// 65,536 tokens of 8 routes: 1.82 ms at 7,168 columns (5.2 TB/s), 0.44 ms at
-// 2,048 (6.1 TB/s; 0.49 with `out` kept in the caches).
+// A row of at most 1,024 columns is one pass of one wave, four tokens to a
+// workgroup; a longer one is shared by the four waves of a workgroup, so that
+// few tokens do not wait for passes one after the other and many read a row's
+// bytes together (W = 1 in brackets, 8 routes): 8 tokens of 7,168 columns 6.3 us
+// (18.2), 1,024 24 (33); 65,536 1.71 ms, 5.5 TB/s (1.82 ms); of 2,048 columns
+// 0.43 ms, 6.2 TB/s (0.44; 0.49 with `out` kept in the caches).  At 4,096 rows of
+// 1,000 columns four waves lose: 12.0 us against 10.0.
 // ---------------------------------------------------------------------------
-template <typename T, int CU, int KB>
+template <typename T, int CU, int KB, int W>
 __global__ __launch_bounds__(256) void k_combine_drop(const u32x4* __restrict__ y,
                                                       const float* __restrict__ gates,
                                                       const int32_t* __restrict__ route,
                                                       const T* residual, const int64_t* rng, T* out,
                                                       int ntok, int K, int hv, uint32_t cut,
                                                       float scale) {
-  const int t = blockIdx.x * 4 + threadIdx.x / kWave;     // whole waves leave together
-  if (t >= ntok) return;
+  const int wv = threadIdx.x / kWave;
+  const int t = W == 1 ? blockIdx.x * 4 + wv : blockIdx.x;
+  if (t >= ntok) return;                                  // whole waves leave together
   const int lane = lane_id();
   DropKey key{};
   if (cut) key = drop_key(rng);
   const int myroute = lane < K ? route[int64_t(t) * K + lane] : -1;
   const float mygate = lane < K ? gates[int64_t(t) * K + lane] : 0.f;
-  for (int c0 = 0; c0 < hv; c0 += kWave * CU) {
+  for (int c0 = W == 1 ? 0 : wv * kWave * CU; c0 < hv; c0 += kWave * CU * W) {
     float acc[CU][8];
 #pragma unroll
     for (int u = 0; u < CU; ++u)
@@ -113,12 +120,13 @@ __global__ __launch_bounds__(256) void k_combine_drop(const u32x4* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// Its gradients: a wave per token draws the numbers of its row once and keeps
-// the masked gradient d in fp32 registers for the K rows (as k_combine_bwd).
-// 65,536 tokens of 8 routes: 3.18 ms at 7,168 columns (5.0 TB/s; 3.23 with dy
-// through the caches), 0.88 ms at 2,048 (5.2 TB/s; 0.92).
+// Its gradients: the numbers of a row are drawn once and the masked gradient d
+// stays in fp32 registers for the K rows (as k_combine_bwd); W as above, the
+// gates' gradients of the waves added in their order.  8 routes: 8 tokens of
+// 7,168 columns 7.4 us (W = 1: 23.5); 65,536 3.15 ms, 5.1 TB/s (3.17; 3.23 with dy
+// through the caches); of 2,048 columns 0.87 ms, 5.2 TB/s (0.88; 0.92).
 // ---------------------------------------------------------------------------
-template <typename T, int CU, int KB>
+template <typename T, int CU, int KB, int W>
 __global__ __launch_bounds__(256) void k_combine_drop_bwd(const T* __restrict__ dout,
                                                           const u32x4* __restrict__ y,
                                                           const float* gates,
@@ -127,15 +135,17 @@ __global__ __launch_bounds__(256) void k_combine_drop_bwd(const T* __restrict__ 
                                                           u32x4* __restrict__ dy, float* dgates,
                                                           int ntok, int K, int hv, uint32_t cut,
                                                           float scale) {
-  const int t = blockIdx.x * 4 + threadIdx.x / kWave;
-  if (t >= ntok) return;
+  __shared__ float s_dot[W][kWave];
+  const int wv = threadIdx.x / kWave;
+  const int t = W == 1 ? blockIdx.x * 4 + wv : blockIdx.x;
+  if (t >= ntok) return;                                  // W > 1: never
   const int lane = lane_id();
   DropKey key{};
   if (cut) key = drop_key(rng);
   const int myroute = lane < K ? route[int64_t(t) * K + lane] : -1;
   const float mygate = lane < K ? gates[int64_t(t) * K + lane] : 0.f;
   float mydot = 0.f;                                      // lane k: dgates[t, k]
-  for (int c0 = 0; c0 < hv; c0 += kWave * CU) {
+  for (int c0 = W == 1 ? 0 : wv * kWave * CU; c0 < hv; c0 += kWave * CU * W) {
     float d[CU][8];
 #pragma unroll
     for (int u = 0; u < CU; ++u) {
@@ -186,6 +196,13 @@ __global__ __launch_bounds__(256) void k_combine_drop_bwd(const T* __restrict__ 
       }
     }
   }
+  if constexpr (W > 1) {
+    s_dot[wv][lane] = mydot;
+    __syncthreads();                                      // gates are read: dgates may be gates
+    if (wv > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) mydot += s_dot[w][lane];
+  }
   if (lane < K) dgates[int64_t(t) * K + lane] = mydot;
 }
 
@@ -203,26 +220,42 @@ static void run_dropout(const void* src, const void* residual, const int64_t* rn
                      static_cast<T*>(dst), groups, cut, scale);
 }
 
-template <typename T, int CU>
+// Calls f(W, CU) as types of the kernels' choice for rows of hv groups.
+template <int N> using Int = std::integral_constant<int, N>;
+template <typename F>
+static void with_shape(int hv, F f) {
+  if (hv <= kWave) f(Int<1>{}, Int<1>{});
+  else if (hv <= 2 * kWave) f(Int<1>{}, Int<2>{});
+  else if (hv <= 4 * kWave) f(Int<4>{}, Int<1>{});
+  else if (hv <= 8 * kWave) f(Int<4>{}, Int<2>{});
+  else f(Int<4>{}, Int<4>{});
+}
+
+template <typename T>
 static void run_combine(const moe_cfg* c, const moe_plan* plan, const moe_bf16* y,
                         const float* gates, const void* residual, const int64_t* rng, void* out,
                         uint32_t cut, float scale, hipStream_t stream) {
   const int ntok = c->R * c->S;
-  hipLaunchKernelGGL((k_combine_drop<T, CU, 4>), dim3((ntok + 3) / 4), dim3(256), 0, stream,
-                     reinterpret_cast<const u32x4*>(y), gates, plan->route,
-                     static_cast<const T*>(residual), rng, static_cast<T*>(out), ntok, c->K,
-                     c->Hp / 8, cut, scale);
+  with_shape(c->Hp / 8, [&](auto W, auto CU) {
+    hipLaunchKernelGGL((k_combine_drop<T, CU(), 4, W()>), dim3(W() == 1 ? (ntok + 3) / 4 : ntok),
+                       dim3(256), 0, stream, reinterpret_cast<const u32x4*>(y), gates, plan->route,
+                       static_cast<const T*>(residual), rng, static_cast<T*>(out), ntok, c->K,
+                       c->Hp / 8, cut, scale);
+  });
 }
 
-template <typename T, int CU>
+template <typename T>
 static void run_combine_bwd(const moe_cfg* c, const moe_plan* plan, const void* dout,
                             const moe_bf16* y, const float* gates, const int64_t* rng, moe_bf16* dy,
                             float* dgates, uint32_t cut, float scale, hipStream_t stream) {
   const int ntok = c->R * c->S;
-  hipLaunchKernelGGL((k_combine_drop_bwd<T, CU, 4>), dim3((ntok + 3) / 4), dim3(256), 0, stream,
-                     static_cast<const T*>(dout), reinterpret_cast<const u32x4*>(y), gates,
-                     plan->route, rng, reinterpret_cast<u32x4*>(dy), dgates, ntok, c->K, c->Hp / 8,
-                     cut, scale);
+  with_shape(c->Hp / 8, [&](auto W, auto CU) {
+    hipLaunchKernelGGL((k_combine_drop_bwd<T, CU(), 4, W()>),
+                       dim3(W() == 1 ? (ntok + 3) / 4 : ntok), dim3(256), 0, stream,
+                       static_cast<const T*>(dout), reinterpret_cast<const u32x4*>(y), gates,
+                       plan->route, rng, reinterpret_cast<u32x4*>(dy), dgates, ntok, c->K,
+                       c->Hp / 8, cut, scale);
+  });
 }
 
 }  // namespace moonep
@@ -270,19 +303,8 @@ extern "C" int moe_combine_dropout(const moe_cfg* cfg, const moe_dropout_cfg* dc
                              {residual == out ? nullptr : residual, bytes},
                              {cut ? rng : nullptr, 16}}))
     return MOE_EINVAL;
-  const int cu = (cfg->Hp / 8 + kWave - 1) / kWave;
-#define MOE_RUN(T, N) \
-  run_combine<T, N>(cfg, plan, y, gates, residual, rng, out, cut, scale, stream)
-  if (dc->f32) {
-    if (cu <= 1) MOE_RUN(float, 1);
-    else if (cu <= 2) MOE_RUN(float, 2);
-    else MOE_RUN(float, 4);
-  } else {
-    if (cu <= 1) MOE_RUN(uint16_t, 1);
-    else if (cu <= 2) MOE_RUN(uint16_t, 2);
-    else MOE_RUN(uint16_t, 4);
-  }
-#undef MOE_RUN
+  const auto run = dc->f32 ? run_combine<float> : run_combine<uint16_t>;
+  run(cfg, plan, y, gates, residual, rng, out, cut, scale, stream);
   return hip_status();
 }
 
@@ -309,18 +331,7 @@ extern "C" int moe_combine_dropout_backward(const moe_cfg* cfg, const moe_dropou
              {cut ? rng : nullptr, 16}}) ||
       overlap(dy, rows * cfg->Hp * 2, gates, rows * 4))
     return MOE_EINVAL;
-  const int cu = (cfg->Hp / 8 + kWave - 1) / kWave;
-#define MOE_RUN(T, N) \
-  run_combine_bwd<T, N>(cfg, plan, dout, y, gates, rng, dy, dgates, cut, scale, stream)
-  if (dc->f32) {
-    if (cu <= 1) MOE_RUN(float, 1);
-    else if (cu <= 2) MOE_RUN(float, 2);
-    else MOE_RUN(float, 4);
-  } else {
-    if (cu <= 1) MOE_RUN(uint16_t, 1);
-    else if (cu <= 2) MOE_RUN(uint16_t, 2);
-    else MOE_RUN(uint16_t, 4);
-  }
-#undef MOE_RUN
+  const auto run = dc->f32 ? run_combine_bwd<float> : run_combine_bwd<uint16_t>;
+  run(cfg, plan, dout, y, gates, rng, dy, dgates, cut, scale, stream);
   return hip_status();
 }

@@ -111,7 +111,8 @@ def plan_of(shape, ids="uniform"):
 @pytest.mark.parametrize("ids", ["uniform", "hot", "failed", "twice"])
 @pytest.mark.parametrize("shape", [
     W.TINY, W.TINY.with_(S=125, Hp=1000), W.TINY.with_(S=1, Hp=8), W.TINY.with_(R=2, B=4, S=33, K=7, Hp=2056),
-    W.TINY.with_(R=1, B=8, S=9, Hp=520), W.TINY.with_(R=1, B=0, mode=1, S=3, E=64, K=64, Hp=72)], ids=str)
+    W.TINY.with_(R=1, B=8, S=9, Hp=520), W.TINY.with_(S=5, Hp=1032), W.TINY.with_(R=1, B=8, S=3, Hp=4104),
+    W.TINY.with_(R=1, B=8, S=2, Hp=8200), W.TINY.with_(R=1, B=0, mode=1, S=3, E=64, K=64, Hp=72)], ids=str)
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
 def test_combine(shape, ids, f32):
     if ids == "twice" and shape.K == 1:
