@@ -687,6 +687,13 @@ __global__ __launch_bounds__(64) void k_join(ProductArgs a) {
   DropKey key{};
   if (a.ep.cut) key = drop_key(a.ep.rng);
   float b[8];
+  // grouped: rows behind the rank's last segment (all, of a failed plan) have no
+  // sums and stay as they were
+  bool live = true;
+  if (a.cu) {
+    const int64_t r = a.first_rank + at / a.SK, per = a.E + a.B;
+    live = at % a.SK < a.cu[r * (per + 1) + per];
+  }
   bias8(a.ep, a.cu ? a.row_expert[at] : 0, a.E, n, b);
   float z[8];
 #pragma unroll
@@ -703,7 +710,7 @@ __global__ __launch_bounds__(64) void k_join(ProductArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] += v[s][i];
   }
-  epilogue8(a.ep, key, z, b, at + int64_t(a.first_rank) * a.SK, n);
+  if (live) epilogue8(a.ep, key, z, b, at + int64_t(a.first_rank) * a.SK, n);
 }
 
 // ---------------------------------------------------------------------------

@@ -237,6 +237,19 @@ def test_failed_plan_writes_nothing():
         k().check()
 
 
+@pytest.mark.parametrize("R,S,E,K,H,Hp,B", [
+    (1, 1, 2, 1, 3176, 24, 0), (1, 664, 2, 1, 4072, 432, 0), (1, 562, 2, 2, 3064, 1808, 0),
+    (1, 905, 2, 1, 6424, 3248, 0), (4, 67, 128, 2, 2296, 16, 32)])
+def test_failed_plan_in_parts_writes_nothing(R, S, E, K, H, Hp, B):
+    """The same where the k axis is cut and the parts are added by a kernel of their own."""
+    s = W.TINY.with_(R=R, S=S, E=E, K=K, H=H, Hp=Hp, B=B, mode=0 if B else 1)
+    ids = W.routing_uniform(s)[0].copy()
+    ids[0, 0] = s.E
+    k = experts(s, O.NONE, ids, pre=True, residual=True)
+    assert np.all(k.expert == -1)
+    k().check()
+
+
 def test_no_rows():
     c = mx.make_cfg(1, 0, 1, 1, 64, 64, 0, mx.MODE_INFER)
     ec = mx.make_epilogue_cfg(O.GELU)
