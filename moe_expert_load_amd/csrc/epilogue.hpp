@@ -268,26 +268,26 @@ __device__ __forceinline__ void epilogue8(const Epilogue& ep, const DropKey& key
   finish8(ep, z, r, at);
 }
 
-// A wave's block of z staged in LDS: groups 0 .. 7 of this lane, group k at
+// A wave's block of z staged in LDS: groups 0 .. NG - 1 of this lane, group k at
 // place(k, at) (its eight values; `at` the flat index of the first in y), null
 // where there is none.  All residuals are asked for before the first group's
 // arithmetic.  The activations are long code: a loop of their own, which leaves
 // the values where they were.  Without one a group goes through in one piece
 // (8,192 x 2,048 x 7,168 with dropout and residual: 264 us by two loops, 251).
-template <typename Place>
+template <int NG, typename Place>
 __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey& key,
                                                Place&& place) {
-  Residual8 r[8];
+  Residual8 r[NG];
   if (ep.residual)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < NG; ++k) {
       int64_t at = 0;
       if (place(k, at)) r[k] = residual8(ep, at);
     }
   const bool plain = ep.act == MOE_ACT_NONE;
   if (!plain)
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < NG; ++k) {
       int64_t at = 0;
       float* p = place(k, at);
       if (!p) continue;
@@ -297,7 +297,7 @@ __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey
       store8(p, z);
     }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < NG; ++k) {
     int64_t at = 0;
     float* p = place(k, at);
     if (!p) continue;

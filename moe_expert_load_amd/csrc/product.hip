@@ -342,26 +342,35 @@ __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
 
 // ---------------------------------------------------------------------------
 // More rows than weights should be read again for, and fewer than fill the chip
-// with 256 x 256 tiles: 128 x 128 tiles, four waves of 64 x 64 (2 x 2 blocks of
-// 32 x 32), operands straight into LDS in stages of 64 k, the k axis cut over
+// with larger tiles: 128 x 128 tiles, four waves of 64 x 64 (2 x 2 blocks of 32 x
+// 32), operands straight into LDS in stages of 64 k, the k axis cut over
 // workgroups as above.  Both operands' rows are whole 128- or 256-byte lines: x
 // [128 rows][64 k] is read with 16-byte LDS reads (chunk kc of row m at kc ^ (m /
 // 2) % 8), the weights [64 k][128 columns] with the transposing read (chunk c of
-// row k at c ^ 4 (k % 4)); neither has a bank conflict.  NST stages: four, with a
-// workgroup of the unit's own; or two, with two workgroups whose loads and
-// epilogues cover each other's products.
+// row k at c ^ 4 (k % 4)); neither has a bank conflict.  A unit holds eight waves
+// with two stages for each four, which together ask LDS for 96 KB a step and four
+// waves: LDS sets the pace (more stages for fewer waves, or one ring of stages for
+// all eight, are no faster).  With G = 1 they are two workgroups, whose loads and
+// epilogues cover each other's products; with G = 2 one, whose groups of four waves
+// share the tile's k axis, add their sums in LDS and do half of its epilogue each:
+// nearly half the steps' time where there are no more tiles than units (2,048 rows of
+// 7,168 onto 384 in 4 parts: 30.8 us, 28.4 by two groups; 4,100 rows over 8 experts
+// of 1,000 x 520: 19.8, 18.3; 188 shapes of up to 256 tiles: 0.91 of the time on
+// average, 1.15 at worst; of 257 to 320 tiles 1.31 to 1.50).
 // ---------------------------------------------------------------------------
 constexpr int kMidTile = 128, kMidStep = 64;
 constexpr int kMidHalf = kMidTile * kMidStep * 2;      // bytes of one operand's stage
 
-template <bool SPLIT>
-__global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
+template <bool SPLIT, int G>
+__global__ __launch_bounds__(256 * G, 2) void k_mid(ProductArgs a) {
   constexpr int NST = 2;
   static_assert(2 * kMidHalf * NST >= 4 * 64 * 256, "the epilogue's staging fits the stages");
-  __shared__ __attribute__((aligned(1024))) unsigned char s_st[NST * 2 * kMidHalf];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_all[G * NST * 2 * kMidHalf];
   RowBlock rb;
   if (!my_block(a, rb)) return;
-  const int lane = lane_id(), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int lane = lane_id(), w8 = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wv = w8 & 3, grp = w8 >> 2;
+  unsigned char* s_st = s_all + grp * NST * 2 * kMidHalf;
   const int wm = wv >> 1, wn = wv & 1;
   const int H = a.H, N = a.ep.N, n0 = rb.n0;
 
@@ -382,7 +391,9 @@ __global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
 
   const u32x4 rx = make_rsrc(a.x + int64_t(rb.row0) * H, uint32_t(rb.rows) * H * 2);
   const u32x4 rw = make_rsrc(weights_of(a, rb), uint32_t(H) * N * 2);
-  const int t0 = first_step(a, rb.split), t1 = first_step(a, rb.split + 1);
+  const int from = first_step(a, rb.split), to = first_step(a, rb.split + 1);
+  const int turns = (to - from + G - 1) / G;              // of the first group, the other's less one
+  const int t0 = from + grp * turns, t1 = min(to, t0 + turns);
 
   // Load u of this wave: x rows 8 (4 wv + u) + lane / 8, weight rows 4 (4 wv +
   // u) + lane / 16.  Past the rows, or past k in the last step, an offset
@@ -417,13 +428,14 @@ __global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
   for (int s = 0; s < NST - 1; ++s)
     if (t0 + s < t1) issue(t0 + s);
 #pragma unroll 1
-  for (int t = t0; t < t1; ++t) {
+  for (int t = t0; t < t0 + turns; ++t) {
     // this wave's loads of stage t have landed; the barrier makes every wave's
     // visible, and says that all are done with the stage that is filled next
     wait_vm<0>();
     // its own LDS reads of the last step are done too, not only asked for
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (t + NST - 1 < t1) issue(t + NST - 1);
+    if (G > 1 && t >= t1) break;                          // the last turn: no barrier follows
     const unsigned char* xs = s_st + (t % NST) * 2 * kMidHalf;
     const unsigned char* ws = xs + kMidHalf;
 #pragma unroll
@@ -449,7 +461,7 @@ __global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
   // 32 x 32 accumulators: lane l holds column l % 32, rows 8 (v / 4) + 4 (l /
   // 32) + v % 4.  Staged in the wave's own 16 KB as 64 rows of 256 bytes (the
   // lane halves, 4 rows apart, swap the row's two column blocks: other banks).
-  unsigned char* cs = s_st + wv * 16384;
+  unsigned char* cs = s_all + w8 * 16384;
   const int half = lane >> 5;
   float bias[2] = {0.f, 0.f};
   DropKey key{};
@@ -466,13 +478,26 @@ __global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         *reinterpret_cast<float*>(cs + (32 * i + 8 * (v >> 2) + 4 * half + (v & 3)) * 256 +
-                                  ((j ^ half) * 128) + (lane & 31) * 4) = acc[i][j][v] + bias[j];
+                                  ((j ^ half) * 128) + (lane & 31) * 4) =
+            G == 1 || grp == 0 ? acc[i][j][v] + bias[j] : acc[i][j][v];
+  if constexpr (G > 1) {
+    // the groups' sums added: each takes half of the rows
+    __syncthreads();
+    cs = s_all + wv * 16384 + grp * 32 * 256;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f32x4* p = reinterpret_cast<f32x4*>(cs + (k * kWave + lane) * 16);
+      const f32x4 o = *reinterpret_cast<const f32x4*>(cs + 4 * 16384 + (k * kWave + lane) * 16);
+      const f32x4 m = *p;
+      *p = f32x4{m[0] + o[0], m[1] + o[1], m[2] + o[2], m[3] + o[3]};
+    }
+  }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   const int n = n0 + wn * 64 + (lane & 7) * 8;
   auto place = [&](int k, int64_t& at) -> float* {
-    const int rr = 8 * k + (lane >> 3), m = wm * 64 + rr;
+    const int rr = 8 * k + (lane >> 3), m = wm * 64 + grp * 32 + rr;
     if (m >= rb.rows || n >= N) return nullptr;
     at = (int64_t(rb.row0) + m) * N + n;
     const int blk = ((lane & 7) >> 2) ^ ((rr >> 2) & 1);
@@ -480,29 +505,32 @@ __global__ __launch_bounds__(256, 2) void k_mid(ProductArgs a) {
   };
   if constexpr (SPLIT) {
     const int64_t first = int64_t(a.first_rank) * a.SK;
-    float* to = a.partial + (int64_t(rb.split) * a.rows - first) * N;
+    float* dst = a.partial + (int64_t(rb.split) * a.rows - first) * N;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 8 / G; ++k) {
       int64_t at = 0;
       const float* p = place(k, at);
       if (!p) continue;
       float z[8];
       load8(p, z);
-      store8(to + at, z);
+      store8(dst + at, z);
     }
-    if (a.cu && rb.split == 0 && n0 == 0 && wn == 0 && wm * 64 + lane < rb.rows)
+    if (a.cu && rb.split == 0 && n0 == 0 && wn == 0 && grp == 0 && wm * 64 + lane < rb.rows)
       a.row_expert[rb.row0 - first + wm * 64 + lane] = expert_of(a.ep, rb.r, rb.j, a.E, a.B);
   } else {
-    epilogue_block(a.ep, key, place);
+    epilogue_block<8 / G>(a.ep, key, place);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Many rows: 128 x 256 tiles, four waves of 64 x 128 (2 x 4 blocks), two
 // workgroups on a unit, so that one's loads and epilogue are covered by the
-// other's products.  LDS bandwidth sets the pace: a tile of this shape reads and
-// fills 72 KB for every 32 k, 1.1 times what the matrix pipe needs to be fed; 128
-// x 128 1.5 times.  The weights go through three stages of 32 k (rows of 512
+// other's products.  A tile of this shape asks LDS for 72 KB every 32 k, 0.75 of
+// what 128 x 128 tiles ask for the same products.  The matrix pipe is 59 % busy at
+// 1.5 GHz (counters, 65,536 rows of 7,168 onto 2,048): power sets the pace, as of
+// the library's product.  That case takes 1.69 to 1.75 ms, 1.1 PFLOP/s (the
+// library's bare product 1.55 to 1.63); 8,192 rows of 2,048 onto 7,168 223 to 230
+// us bare, 251 with dropout and residual.  The weights go through three stages of 32 k (rows of 512
 // bytes); x, whose rows of 32 k would be half lines, in pairs of steps through
 // two buffers: 80 KB a workgroup.
 // ---------------------------------------------------------------------------
@@ -667,7 +695,7 @@ __global__ __launch_bounds__(256, 2) void k_wide(ProductArgs a) {
         store8(to + at, z);
       }
     } else {
-      epilogue_block(a.ep, key, place);
+      epilogue_block<8>(a.ep, key, place);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -729,7 +757,8 @@ __global__ __launch_bounds__(64) void k_join(ProductArgs a) {
 // Fitted (non-negative least squares of the relative error) to 8,384 timings of
 // 416 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
 // 7,168, one to 384 experts.  The median error is 3 to 5 %; what the model picks
-// was 1.9 % slower than the best of them on average, 38 % at worst.
+// was 1.9 % slower than the best of them on average, 38 % at worst; of 368 further
+// shapes 1.9 % and 44 %.
 struct Tile {
   int height, cols, step_k, waves, at_once;
   float start, step, half, round, filled, join, part, sums, store, list, weight;
@@ -746,6 +775,7 @@ constexpr Tile kTiles[4] = {
 };
 constexpr int kMostSplits = 32;          // parts of the k axis
 constexpr int64_t kMostItems = (1 << 24) - 8;  // a launch holds fewer than 2^32 threads
+constexpr int64_t kUnits = 256;          // compute units
 constexpr int64_t kSplitItems = 512;     // a split call fills the chip about once
 constexpr int64_t kCached = 256 << 20;   // bytes that the last cache holds
 constexpr int64_t kOnceRows = 4;         // mean rows of a segment that is about one block
@@ -822,7 +852,9 @@ static void run_product(const ProductArgs& a, int tile, bool once, hipStream_t s
   else if (tile == 0) hipLaunchKernelGGL((k_few<1, SPLIT, false>), grid, block, 0, stream, a);
   else if (tile == 1 && once) hipLaunchKernelGGL((k_few<2, SPLIT, true>), grid, block, 0, stream, a);
   else if (tile == 1) hipLaunchKernelGGL((k_few<2, SPLIT, false>), grid, block, 0, stream, a);
-  else if (tile == 2) hipLaunchKernelGGL((k_mid<SPLIT>), grid, block, 0, stream, a);
+  else if (tile == 2 && items <= kUnits)
+    hipLaunchKernelGGL((k_mid<SPLIT, 2>), grid, dim3(512), 0, stream, a);
+  else if (tile == 2) hipLaunchKernelGGL((k_mid<SPLIT, 1>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((k_wide<SPLIT>), grid, block, 0, stream, a);
 }
 

@@ -207,6 +207,10 @@ def test_experts(shape, ids, ranks):
     (1, 37, 16, 1, 2440, 3496, 0), (1, 18, 16, 2, 5072, 1680, 0),             # 32 rows past the caches; in 2
     (1, 944, 2, 2, 432, 1312, 0), (1, 562, 2, 2, 3064, 1808, 0),              # 128 x 128; in 3
     (1, 3570, 2, 2, 376, 6352, 0), (1, 905, 2, 1, 6424, 3248, 0),             # 128 x 256; in 3
+    # 128 x 128 by two groups of waves: whole (one, three and 16 steps), in 8 parts; by two workgroups a unit
+    (1, 5660, 4, 1, 32, 512, 0), (1, 2830, 4, 2, 176, 560, 0), (1, 2744, 1, 1, 160, 1144, 0),
+    (1, 4100, 8, 1, 1000, 520, 0), (1, 3749, 1, 1, 2584, 24, 0), (1, 1713, 4, 2, 4152, 40, 0),
+    (1, 2609, 1, 1, 264, 1920, 0), (1, 5285, 8, 1, 128, 1328, 0),
     (8, 1, 128, 2, 496, 32, 16), (4, 67, 128, 2, 2296, 16, 32),               # by a list: 16 rows; in 3
     (4, 31, 128, 2, 2120, 152, 32), (4, 5, 128, 2, 856, 1424, 32),            # 32 rows; past the caches
     (4, 5, 128, 2, 2608, 480, 32), (4, 293, 128, 2, 40, 176, 32),             # 32 rows in 3; 128 x 128
