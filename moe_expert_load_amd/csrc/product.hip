@@ -186,8 +186,9 @@ __device__ __forceinline__ void give8(const ProductArgs& a, const RowBlock& rb, 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: the single tokens of decoding, the router.  The time is that of
-// reading the weights once, so they go from memory to registers and nowhere else.
+// Few rows: the single tokens of decoding, one matrix or an expert each.  The time
+// is that of reading the weights once, so they go from memory to registers and
+// nowhere else.
 // A wave takes 128 columns and steps of 32 k.  Lane l loads rows k0 + 8 (l / 16) +
 // 0 .. 7 of columns n0 + 8 (l % 16) + 0 .. 7, eight 16-byte loads of which every 16
 // lanes cover 256 contiguous bytes.  A matrix instruction wants eight consecutive
@@ -530,9 +531,9 @@ __global__ __launch_bounds__(256 * G, 2) void k_mid(ProductArgs a) {
 // 1.5 GHz (counters, 65,536 rows of 7,168 onto 2,048): power sets the pace, as of
 // the library's product.  That case takes 1.69 to 1.75 ms, 1.1 PFLOP/s (the
 // library's bare product 1.55 to 1.63); 8,192 rows of 2,048 onto 7,168 223 to 230
-// us bare, 251 with dropout and residual.  The weights go through three stages of 32 k (rows of 512
-// bytes); x, whose rows of 32 k would be half lines, in pairs of steps through
-// two buffers: 80 KB a workgroup.
+// us bare, 251 with dropout and residual.  The weights go through three stages of
+// 32 k (rows of 512 bytes); x, whose rows of 32 k would be half lines, in pairs of
+// steps through two buffers: 80 KB a workgroup.
 // ---------------------------------------------------------------------------
 constexpr int kWideCols = 256, kWideStep = 32;
 constexpr int kWidePair = 128 * 64 * 2, kWideW = kWideStep * kWideCols * 2;
