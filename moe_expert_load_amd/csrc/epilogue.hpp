@@ -133,7 +133,7 @@ __device__ __forceinline__ void act_grad8(float (&d)[8], const float (&z)[8], in
     }
   } else if (act == MOE_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = z[i] > 0.f ? d[i] : z[i] == z[i] ? 0.f : z[i];
+    for (int i = 0; i < 8; ++i) d[i] *= z[i] > 0.f ? 1.f : z[i] == z[i] ? 0.f : z[i];
   } else if (act == MOE_ACT_RELU2) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] *= z[i] < 0.f ? 0.f : 2.f * z[i];
