@@ -585,6 +585,8 @@ def _plan_or_none(cfg, plan, dev):
     if plan is None:
         return None
     _arg(plan.cu_seqlens, torch.int32, cfg.R * (cfg.E + cfg.B + 1), "plan", dev)
+    if cfg.B:
+        _arg(plan.slot_expert, torch.int32, cfg.R * cfg.B, "the plan's slots", dev)
     return plan.c
 
 
