@@ -481,6 +481,12 @@ def moe_router_backward(cfg, rcfg, logits, topk_ids, dgates, cu_tokens, counts, 
         _arg(dlogits, dtype, T * cfg.E, "dlogits", dev), _on(stream, dev)), "moe_router_backward")
 
 
+def _fits(rows, width, where):
+    """Refuses what the library's int64 and int32 would cut to its low bits."""
+    if not (-(1 << 63) <= rows < 1 << 63 and -(1 << 31) <= width < 1 << 31):
+        raise MoeError(MOE_ELIMIT, where)
+
+
 def _kept(rows, width, q, scale, what, dev):
     """Codes and scale bytes of `rows` rows of `width` values."""
     return (_arg(q, torch.uint8, rows * width, what + " codes", dev),
@@ -489,6 +495,7 @@ def _kept(rows, width, q, scale, what, dev):
 
 def moe_q8_store(rows, width, src, q, scale, stream=None):
     """Codes q [rows, width] and scale bytes [rows, ceil(width / 32)] of bf16 rows."""
+    _fits(rows, width, "moe_q8_store")
     dev = torch.cuda.current_device()
     _check(load().moe_q8_store(rows, width,
                                _arg(src, torch.bfloat16, rows * width, "src", dev),
@@ -497,6 +504,7 @@ def moe_q8_store(rows, width, src, q, scale, stream=None):
 
 
 def moe_q8_load(rows, width, q, scale, dst, stream=None):
+    _fits(rows, width, "moe_q8_load")
     dev = torch.cuda.current_device()
     _check(load().moe_q8_load(rows, width, *_kept(rows, width, q, scale, "q8", dev),
                               _arg(dst, torch.bfloat16, rows * width, "dst", dev),
@@ -629,6 +637,7 @@ def moe_epilogue_backward(cfg, ecfg, plan, dy, pre, rng, dz, dbias, workspace=No
 
 def moe_dropout(dcfg, rows, width, src, residual, rng, dst, stream=None):
     """dst = residual + dropout(src); residual may be None."""
+    _fits(rows, width, "moe_dropout")
     dev = torch.cuda.current_device()
     n, to = rows * width, _row_type(dcfg.f32)
     _check(load().moe_dropout(
