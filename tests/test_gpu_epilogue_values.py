@@ -1,15 +1,15 @@
 """Values of the product with an epilogue and of its backward that are known without a tolerance
-of their own: infinities, NaN and zeros.
+of their own: infinities, NaN and zeros in every row.
 """
 import numpy as np
 import pytest
 import torch
 
 import moe_expert_load_amd as mx
-from epilogue_checks import R, close
+from epilogue_checks import R, close, h
 from gpu_helpers import announce, free
 from oracle import epilogue as O
-from test_gpu_epilogue import Out, f64, workspace
+from test_gpu_epilogue import Out, f64, matrix, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -32,6 +32,31 @@ def same(got, want, tol, what):
     assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], want[inf]), what
     ok = np.isfinite(want)
     close(got[ok], want[ok], np.broadcast_to(tol, want.shape)[ok], what)
+
+
+# every tile of the product, with the k axis whole and in parts
+@pytest.mark.parametrize("S,H,Hp", [(3, 16, 8), (1300, 16, 8), (2, 728, 24), (13, 7160, 392), (943, 360, 1080),
+                                    (567, 3376, 536), (2406, 432, 824), (1485, 3824, 1392), (4100, 1000, 520),
+                                    (6881, 360, 7016), (653, 7064, 5520)])
+@pytest.mark.parametrize("kind", range(6))
+def test_special_values_in_every_row(S, H, Hp, kind):
+    """The values as bias on zero products: each row is the function of the bias.
+
+    The share that a function multiplies by is 0 or 1 here, off by one unit of the hardware
+    reciprocal, 2 h, and the product by h; squares and pre are rounded once.
+    """
+    vals = np.array([INF, -INF, NAN, 0.0, -0.0, 1e30, -1e30, 3e38])
+    k = matrix(S, H, Hp, kind, f32=True, pre=True, seed=1)
+    k.x.zero_()
+    k.bias[0] = torch.from_numpy(np.resize(vals, Hp)).float()
+    k()
+    k.y.check()
+    k.pre.check()
+    z = f64(k.bias)[0]
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = O.act(z, kind).astype(np.float32).astype(np.float64)
+        same(f64(k.y.t), want[None], 4 * h * np.abs(want)[None], "y")
+        same(f64(k.pre.t), z[None], R * np.abs(z)[None], "pre")
 
 
 @pytest.mark.parametrize("S", [1, 9, 5000])
