@@ -1,5 +1,5 @@
 """Values of the product with an epilogue and of its backward that are known without a tolerance
-of their own: infinities, NaN and zeros in every row.
+of their own: infinities, NaN and zeros in every row, and sums of whole numbers past 2^31 values.
 """
 import numpy as np
 import pytest
@@ -9,7 +9,7 @@ import moe_expert_load_amd as mx
 from epilogue_checks import R, close, h
 from gpu_helpers import announce, free
 from oracle import epilogue as O
-from test_gpu_epilogue import Out, f64, matrix, workspace
+from test_gpu_epilogue import Out, f64, matrix, rng_of, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,34 @@ def test_gradients_that_are_not_finite(kind, S):
     finite = np.isfinite(want)
     assert np.array_equal(np.isfinite(f64(db.t))[0], finite)
     assert np.array_equal(np.isnan(f64(db.t))[0], np.isnan(want))
+
+
+def test_bias_gradients_past_32_bits():
+    """More than 2^31 values without an activation, dy 1/2 and half of them dropped: dz is 0 or
+    1, so the biases' gradients are counts below 2^24, which fp32 sums without an error."""
+    E, Hp, S = 4, 2048, (1 << 31) // 2048 // 4 + 176
+    announce("bias gradients past 32 bits", E, Hp, S)
+    c = mx.make_cfg(4, S, E, 1, 8, Hp, 0, mx.MODE_INFER)     # S Hp 2 < 4 GiB a rank
+    plan = mx.Plan(c)
+    # every rank has rows of every expert, cut anywhere, one segment without rows, and a rest
+    cu = torch.tensor([[0, 3, 100003, 100003, S], [0, 0, 131071, 131099, S - 5], [0, S // 2, S // 2 + 1, S - 1, S],
+                       [0, 77777, 155555, 200000, S - 300]], dtype=torch.int32)
+    plan.cu_seqlens[:20].copy_(cu.reshape(-1))
+    ec = mx.make_epilogue_cfg(O.NONE, 0.5)
+    dy = torch.full((4 * S, Hp), 0.5, dtype=torch.bfloat16, device="cuda")
+    assert dy.numel() > 1 << 31
+    db, rng = torch.empty((E, Hp), device="cuda"), rng_of(12, 34)
+    mx.moe_epilogue_backward(c, ec, plan, dy, None, rng, dy, db, workspace(c, ec))
+    torch.cuda.synchronize()
+    rows = 4 * S
+    at = np.concatenate([np.arange(4), np.arange(rows // 2 - 2, rows // 2 + 2), np.arange(rows - 4, rows)])
+    got = f64(dy.index_select(0, torch.from_numpy(at).cuda()))
+    assert np.array_equal(got, 0.5 * O.row_factor(0.5, [12, 34], at, Hp))
+    for e in range(E):
+        count = torch.zeros(Hp, dtype=torch.int64, device="cuda")
+        for r in range(4):
+            lo, hi = (r * S + int(v) for v in cu[r, e:e + 2])
+            for a in range(lo, hi, 1 << 15):
+                count += (dy[a:min(hi, a + (1 << 15))] != 0).sum(0)
+        assert int(count.max()) < 1 << 24
+        assert torch.equal(db[e].double(), count.double()), e
