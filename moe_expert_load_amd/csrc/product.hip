@@ -40,7 +40,7 @@ struct ProductArgs {
   int32_t H, E, B, SK, first_rank, nranks;
   int32_t rows, height, cols, strips, steps, splits;
   int32_t blocks;            // grouped: the most there may be
-  int32_t once;              // about one block for each segment, weights not in the caches
+  int32_t once;              // about one block for each segment, all weights too many to be kept
   Epilogue ep;
 };
 
@@ -212,14 +212,18 @@ __device__ __forceinline__ void column_pair(const u32x4 (&w)[8], int j, bf16x8& 
   odd = __builtin_bit_cast(bf16x8, o);
 }
 
-// RB: blocks of 16 rows that a workgroup takes.  ONCE: weights that are too many
-// for the caches, and read by about one block each, pass them by, and strips are
-// taken over the experts in turn (my_block).  One token on each of 8 ranks, 41
-// experts of 7,168 x 2,048 met: 224 us through the caches expert by expert, 209
-// strip by strip, 201 past them, 189 both (6.3 TB/s).  Not so where blocks share
-// weights (568 rows over 60 experts of 880 x 6,576: 116, 154, 133, 171) or where
-// the last cache holds them from call to call (64 experts of 1,024 x 512: 10, 10,
-// 13, 12).
+// RB: blocks of 16 rows that a workgroup takes.  ONCE: where the experts' weights
+// are too many for the last cache, and read by about one block each, they pass it
+// by, and strips are taken over the experts in turn (my_block).  One token on each
+// of 8 ranks, 41 experts of 7,168 x 2,048 met: 224 us through the caches expert by
+// expert, 209 strip by strip, 201 past them, 189 both (6.3 TB/s).  Not so where
+// blocks share weights (568 rows over 60 experts of 880 x 6,576: 116, 154, 133, 171)
+// or where the last cache holds them from call to call (64 experts of 1,024 x 512:
+// 10, 10, 13, 12).  All experts' weights count, not only those that a call meets: a
+// later call meets others, or comes after other layers.  One token on 8 of 384
+// experts of 1,024 x 512 (8 MB of 403) after other work 16 us (through the caches
+// 17), with other experts from call to call 12 (13.6), with the same ones 8 to 12 (8);
+// on 8 of 24 of 2,648 x 2,160 (92 MB of 275) 28 (42), 25 (22), 25 (20).
 template <int RB, bool SPLIT, bool ONCE>
 __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
   __shared__ f32x4 s_sum[4 * 3 * RB * kWave * 2];
@@ -785,7 +789,7 @@ constexpr int64_t kOnceRows = 4;         // mean rows of a segment that is about
 struct ProductPlan {
   int64_t rows;
   int tile, blocks, strips, steps, splits;
-  bool once;      // the weights are not in the caches, and are read by one block each
+  bool once;      // the experts' weights are too many to be kept, and are read by one block each
 };
 
 static ProductPlan product_plan(const moe_cfg* c, bool dense, int64_t nranks) {
