@@ -761,9 +761,17 @@ __global__ __launch_bounds__(64) void k_join(ProductArgs a) {
 //   + list + weights of the segments with rows / 2^20 * weight    for experts.
 // Fitted (non-negative least squares of the relative error) to 8,384 timings of
 // 416 shapes on one MI355X: one to 16,384 rows (a few to 65,536), widths of 8 to
-// 7,168, one to 384 experts.  The median error is 3 to 5 %; what the model picks
-// was 1.9 % slower than the best of them on average, 38 % at worst; of 368 further
-// shapes 1.9 % and 44 %.
+// 7,168, one to 384 experts; of products with a bias and nothing else, replayed with
+// the same inputs, and of 128 x 128 tiles by one group of waves only, also where two
+// are launched now.  Against the kernels as they are, 169 other shapes (3,135
+// timings): the median error is 3.4, 3.9, 8.3 and 5.1 % in the order of the rows,
+// what the model picks is 2.6 % slower than the best of them on average, 61 % at
+// worst.  With gelu, dropout, residual and z kept (120 shapes, 2,414 timings) times
+// are 10 % longer than modelled, all kernels' alike but for the last one's 6 %, and
+// the pick costs 2.7 % on average, 54 % at worst.  Large calls, which power holds
+// back, take longer too: 8,192 rows of 2,048 onto 7,168 with dropout and residual 250
+// to 281 us, by the model 199; 65,536 of 7,168 onto 2,048 over 48 experts 2.0 to 2.2
+// ms, by the model 1.4.
 struct Tile {
   int height, cols, step_k, waves, at_once;
   float start, step, half, round, filled, join, part, sums, store, list, weight;
