@@ -700,7 +700,8 @@ int moe_grouped_gemm_epilogue(const moe_cfg *cfg, const moe_epilogue_cfg *ec,
  * for it.  Either may be NULL, not both; pre may be NULL with MOE_ACT_NONE; plan
  * is read only for dbias and may be NULL without it, or as above.  The
  * gradient by the residual is dy itself.  At z = 0 the slope of MOE_ACT_RELU is
- * 0.  dz may be pre, or dy if that is bf16 (in place); apart from that dz, dbias
+ * 0; a slope of 0 is multiplied like any other, so an infinite or NaN dy gives
+ * NaN there.  dz may be pre, or dy if that is bf16 (in place); apart from that dz, dbias
  * and the workspace must not overlap each other or the inputs.
  */
 int moe_epilogue_backward(const moe_cfg *cfg, const moe_epilogue_cfg *ec, const moe_plan *plan,
