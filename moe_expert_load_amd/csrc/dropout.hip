@@ -14,7 +14,8 @@ namespace moonep {
 // ---------------------------------------------------------------------------
 // dst = residual + dropout(src): a lane takes groups of eight values, U of them
 // with their loads in flight together.  dst may be src or residual.
-// 65,536 rows of 7,168 with a residual, bf16: 0.45 to 0.47 ms (6.0 TB/s); 8 rows: 3 us.
+// 65,536 rows of 7,168 with a residual, bf16: 0.46 to 0.48 ms (6.0 TB/s), 0.48 to 0.51
+// in the first launches after a pause; 8 rows: 3 us.
 // ---------------------------------------------------------------------------
 template <typename T, int U>
 __global__ __launch_bounds__(256) void k_dropout(const T* src, const T* residual,
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(256) void k_dropout(const T* src, const T* residual
 // workgroup; a longer one is shared by the four waves of a workgroup, so that
 // few tokens do not wait for passes one after the other and many read a row's
 // bytes together (W = 1 in brackets, 8 routes): 8 tokens of 7,168 columns 6.3 us
-// (18.2), 1,024 24 (33); 65,536 1.71 ms, 5.5 TB/s (1.82 ms); of 2,048 columns
+// (18.2), 1,024 24 (33); 65,536 1.71 to 1.76 ms, 5.4 TB/s (1.82 ms); of 2,048 columns
 // 0.43 ms, 6.2 TB/s (0.44; 0.49 with `out` kept in the caches).  At 4,096 rows of
 // 1,000 columns four waves lose: 12.0 us against 10.0.
 // ---------------------------------------------------------------------------
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(256) void k_combine_drop(const u32x4* __restrict__ 
 // Its gradients: the numbers of a row are drawn once and the masked gradient d
 // stays in fp32 registers for the K rows (as k_combine_bwd); W as above, the
 // gates' gradients of the waves added in their order.  8 routes: 8 tokens of
-// 7,168 columns 7.4 us (W = 1: 23.5); 65,536 3.15 ms, 5.1 TB/s (3.17; 3.23 with dy
+// 7,168 columns 7.4 us (W = 1: 23.5); 65,536 3.15 to 3.18 ms, 5.0 TB/s (3.17; 3.23 with dy
 // through the caches); of 2,048 columns 0.87 ms, 5.2 TB/s (0.88; 0.92).
 // ---------------------------------------------------------------------------
 template <typename T, int CU, int KB, int W>

@@ -55,7 +55,8 @@ __device__ __forceinline__ int segment_of(const int32_t* cu, int n, int row) {
 // Blocks of 4 U rows, U a wave: their loads go out first, before the block's
 // segments are known and before any of them is stored, so dz may be what is read.
 // 524,288 rows of 2,048 over 384 experts, gelu, bf16, in cold memory 1.24 to 1.32
-// ms with dropout (5.2 to 4.9 TB/s); 3 % more through the caches.
+// ms with dropout (5.2 to 4.9 TB/s), up to 1.5 in the first ten launches after a pause;
+// 3 % more through the caches.
 template <typename D, int U>
 __global__ __launch_bounds__(256) void k_eb(EbArgs a) {
   __shared__ f32x4 s_sum[3][2][kWave];

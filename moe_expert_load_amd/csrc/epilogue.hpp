@@ -171,7 +171,7 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 
 // The same past the caches, for tensors that a pass reads or writes once: a
 // stream that stays in the caches costs the others their place (65,536 x 7,168
-// dropped and added, bf16: 0.488 ms through them, 0.446 past them).
+// dropped and added, bf16: 0.49 ms through them, 0.46 to 0.47 past them).
 __device__ __forceinline__ void load8_once(const uint16_t* p, float (&v)[8]) {
   const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
@@ -227,8 +227,9 @@ __device__ __forceinline__ Residual8 residual8(const Epilogue& ep, int64_t at) {
   return r;
 }
 
-// z + residual, rounded once, to y (8,192 x 2,048 x 7,168 with dropout and residual:
-// 290 us with y through the caches, 276 past them).
+// z + residual, rounded once, to y (8,192 x 2,048 x 7,168 with dropout and residual,
+// one launch after another: 271 to 278 us with y through the caches, 261 to 268 past
+// them; with new inputs each time 278 to 284 and 272 to 279).
 __device__ __forceinline__ void finish8(const Epilogue& ep, float (&z)[8], const Residual8& r,
                                         int64_t at) {
   if (ep.f32) {
@@ -273,7 +274,8 @@ __device__ __forceinline__ void epilogue8(const Epilogue& ep, const DropKey& key
 // where there is none.  All residuals are asked for before the first group's
 // arithmetic.  The activations are long code: a loop of their own, which leaves
 // the values where they were.  Without one a group goes through in one piece
-// (8,192 x 2,048 x 7,168 with dropout and residual: 264 us by two loops, 251).
+// (8,192 x 2,048 x 7,168 with dropout and residual, one launch after another: 267 to
+// 273 us by two loops, 261 to 268; with new inputs 287 to 291, 272 to 279).
 template <int NG, typename Place>
 __device__ __forceinline__ void epilogue_block(const Epilogue& ep, const DropKey& key,
                                                Place&& place) {

@@ -85,10 +85,13 @@ struct RowBlock {
 // What this workgroup multiplies; false: nothing.  Neighbouring items go to one
 // XCD: the row blocks of a band of a segment under one strip of columns, then the
 // next strip, so that what an XCD's units work on at a time is about square and
-// its L2 reads the fewest rows and columns for it.  A segment is cut into even
-// bands of 6 to 11 blocks (65,536 rows of 7,168 onto 2,048: bands of 4, 8, 16 and
-// 32 blocks take 1.70, 1.69, 1.73 and 1.95 ms; over 48 experts of 11 blocks each,
-// bands of 8 that straddle them 1.95 ms, of 11 1.89).
+// its L2 reads the fewest rows and columns for it.  A segment is cut into bands of
+// 6 to 11 blocks, all of one size but the last, which has what is left: one block
+// at least (65,536 rows of 7,168 onto 2,048: bands of 4, 8, 16 and 32 blocks take
+// 1.70, 1.69, 1.73 and 1.95 ms; over 48 experts of 11 blocks each, bands of 8 that
+// straddle them 1.95 ms, of 11 1.89).  Bands that differ by one block at most, in
+// place of a short last one, change nothing: segments of 33 to 257 blocks with a
+// last band of 1 to 7, both ways round of 7,168 x 2,048, within 1 % on either side.
 //
 // Where the segments are few every wave counts their blocks itself, kScan
 // segments a lane: 1 us, where the list of k_row_blocks costs 4 and a launch.
@@ -359,8 +362,9 @@ __global__ __launch_bounds__(256, 2) void k_few(ProductArgs a) {
 // epilogues cover each other's products; with G = 2 one, whose groups of four waves
 // share the tile's k axis, add their sums in LDS and do half of its epilogue each:
 // nearly half the steps' time where there are no more tiles than units (2,048 rows of
-// 7,168 onto 384 in 4 parts: 30.8 us, 28.4 by two groups; 4,100 rows over 8 experts
-// of 1,000 x 520: 19.8, 18.3; 188 shapes of up to 256 tiles: 0.91 of the time on
+// 7,168 onto 384 in 4 parts, in fp32: 29.7 us, 27.3 by two groups, joins included;
+// 4,100 rows over 8 experts of 1,000 x 520 with everything in the epilogue: 23.9,
+// 20.6; both replayed.  Bare, 188 shapes of up to 256 tiles: 0.91 of the time on
 // average, 1.15 at worst; of 257 to 320 tiles 1.31 to 1.50).
 // ---------------------------------------------------------------------------
 constexpr int kMidTile = 128, kMidStep = 64;
@@ -534,10 +538,12 @@ __global__ __launch_bounds__(256 * G, 2) void k_mid(ProductArgs a) {
 // what 128 x 128 tiles ask for the same products.  The matrix pipe is 59 % busy at
 // 1.5 GHz (counters, 65,536 rows of 7,168 onto 2,048): power sets the pace, as of
 // the library's product.  That case takes 1.69 to 1.75 ms, 1.1 PFLOP/s (the
-// library's bare product 1.55 to 1.63); 8,192 rows of 2,048 onto 7,168 223 to 230
-// us bare, 251 with dropout and residual.  The weights go through three stages of
-// 32 k (rows of 512 bytes); x, whose rows of 32 k would be half lines, in pairs of
-// steps through two buffers: 80 KB a workgroup.
+// library's bare product 1.55 to 1.63); 8,192 rows of 2,048 onto 7,168 223 to 242
+// us bare (the library's 200 to 213), 250 to 268 with dropout and residual.  Those
+// are launches one after another; the first 40 or so after a pause take 270 to 310
+// while the clock settles, and a call among others with new inputs 272 to 281.  The
+// weights go through three stages of 32 k (rows of 512 bytes); x, whose rows of 32 k
+// would be half lines, in pairs of steps through two buffers: 80 KB a workgroup.
 // ---------------------------------------------------------------------------
 constexpr int kWideCols = 256, kWideStep = 32;
 constexpr int kWidePair = 128 * 64 * 2, kWideW = kWideStep * kWideCols * 2;
