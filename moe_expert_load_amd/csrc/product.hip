@@ -91,7 +91,7 @@ struct RowBlock {
 // 1.70, 1.69, 1.73 and 1.95 ms; over 48 experts of 11 blocks each, bands of 8 that
 // straddle them 1.95 ms, of 11 1.89).  Bands that differ by one block at most, in
 // place of a short last one, change nothing: segments of 33 to 257 blocks with a
-// last band of 1 to 7, both ways round of 7,168 x 2,048, within 1 % on either side.
+// last band of 1 to 6, both ways round of 7,168 x 2,048, within 1 % on either side.
 //
 // Where the segments are few every wave counts their blocks itself, kScan
 // segments a lane: 1 us, where the list of k_row_blocks costs 4 and a launch.
